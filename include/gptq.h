@@ -20,7 +20,8 @@
  *    is DEVICE memory owned by the caller.  The library never allocates or
  *    frees device memory.  Host-side validation happens before any CUDA call:
  *    an invalid argument returns an error code and launches nothing.
- *  - Matrices are dense, row-major, with no padding (row stride = columns).
+ *  - Matrices are dense, row-major, with no padding (row stride = columns),
+ *    except where a call takes a leading dimension (ld...).
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Calls only enqueue work; they return before it runs.
  *  - Errors found on the device (a non-positive pivot, non-finite values, a
@@ -28,7 +29,8 @@
  *    gptq_get_status() synchronizes the stream, returns it and clears it.
  *    No kernel traps, asserts or waits without a bound.
  *  - Sizes: d_in must be a multiple of 128 and at most 32768; d_out >= 1;
- *    pointers to float / uint32 data must be 16-byte aligned.
+ *    pointers to float / uint32 data must be 16-byte aligned (the 8-bit
+ *    floating-point calls and the token scores state their own rules).
  *  - Calls on different streams may run concurrently if they touch
  *    different buffers and workspaces; the status word is shared.
  */
@@ -53,7 +55,7 @@ typedef enum {
     GPTQ_ERR_CUDA = 7           /* a CUDA runtime call failed                 */
 } gptq_status;
 
-typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1 } gptq_dtype;
+typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2 } gptq_dtype;
 
 /* Version of this ABI (bumped on any incompatible change). */
 int gptq_abi_version(void);
@@ -353,6 +355,104 @@ int gptq_dequant_gemv(const uint32_t* codes, const uint16_t* scales, const uint1
 int gptq_dequantize(const uint32_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_out,
                     int64_t d_in, int bits, int groupsize, const int32_t* perm, int out_dtype, void* out,
                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit floating-point form -- e4m3 codes with one fp32 scale per block.
+ * Source: note "Model Quantization", "주요 양자화 기법" (FP8 beside GPTQ and
+ * AWQ among the post-training forms).  The pages give no arithmetic for it;
+ * this is the block-scaled form: along the input channels a scale covers 128
+ * values of one token, or 128 x 128 weights.
+ *
+ *   a = max |x| over the block;  s = RN(max(a, 2^-90) / 448)  (fp32);
+ *   c = the real quotient x / s rounded once to e4m3 (half to even), at most
+ *       448 in magnitude.  A block that holds a NaN or an infinity gets the
+ *       scale NaN and NaN codes, and GPTQ_ERR_NONFINITE is recorded with the
+ *       token (weights: the block's first row) as its detail.
+ *
+ * Here rows may be pitched and no size need be a multiple of anything:
+ *   dtype   GPTQ_F32, GPTQ_BF16 or GPTQ_F16 (x, W), aligned to its size.
+ *   ldx, ldw    elements between rows, >= d_in.
+ *   codes   uint8 e4m3 bit patterns, 16-byte aligned; ldc bytes between rows,
+ *           a multiple of 16, >= d_in.  The bytes of a row behind d_in are not
+ *           written (and not read by the products).
+ *   scales  fp32, 4-byte aligned, blocks = ceil(d_in / 128).
+ *     rows:    scales[b * lds + t], block b of token t; lds >= m.
+ *     weight:  scales[(r / 128) * blocks + b], dense [ceil(d_out / 128), blocks].
+ * Sizes: 0 <= m <= 2^24 (m = 0: nothing to do), 1 <= d_out <= 2^22,
+ * 1 <= d_in <= 2^18; pitches up to 2^36.  An output may not overlap an input
+ * or another output; an array reaches from its first to its last element, so
+ * pitched rows that interleave with another array's count as overlapping.
+ * ---------------------------------------------------------------------- */
+int gptq_fp8_quantize_rows(const void* x, int dtype, int64_t m, int64_t d_in, int64_t ldx,
+                           uint8_t* codes, int64_t ldc, float* scales, int64_t lds, void* stream);
+int gptq_fp8_quantize_weight(const void* W, int dtype, int64_t d_out, int64_t d_in, int64_t ldw,
+                             uint8_t* codes, int64_t ldc, float* scales, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products of the 8-bit form (source as above), for one token as for a batch
+ * of prompts.
+ *
+ *   y[t][r] = sum_b xs[b][t] ws[r / 128][b] sum_{k in block b} x[t][k] w[r][k]
+ *
+ * with the codes' values on the right; products of codes are exact, the sum
+ * inside a block and the sum over blocks are fp32, and y is rounded once to
+ * its type.
+ *
+ * gptq_fp8_gated: the first half of a gated feed-forward layer,
+ *   h[t][r] = act(g[t][r]) u[t][r],  g and u the products with Wg and Wu,
+ * in one kernel: neither product is written.  h leaves as values, or
+ * (out = GPTQ_FP8) as the codes and scales that gptq_fp8_quantize_rows would
+ * give for the fp32 values, ready for the next product.
+ *
+ *   x       codes [m, d_in], pitch ldx; xs [blocks, m], pitch lds.
+ *   w, Wg, Wu   codes [d_out, d_in], pitch ldw (both weights of a gated pair);
+ *           ws, gs, us dense [ceil(d_out / 128), blocks].
+ *           Alignment and pitches of codes and scales as above.
+ *   out     the type of y: GPTQ_F32, GPTQ_BF16, GPTQ_F16; gptq_fp8_gated also
+ *           GPTQ_FP8.  ldy: elements between rows of y, >= d_out; y aligned
+ *           to its type's size (codes: as above).
+ *   ys      GPTQ_FP8: scales of h, [ceil(d_out / 128), m], pitch ldys >= m;
+ *           otherwise NULL.
+ *   act     0: silu, g / (1 + e^-g).  1: gelu, g Phi(g) (the exact form).
+ * Sizes and overlaps as above.  Deterministic: the same call
+ * gives the same bits; no workspace.
+ * ---------------------------------------------------------------------- */
+#define GPTQ_FP8 3
+int gptq_fp8_gemm(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, const uint8_t* w, int64_t ldw,
+                  const float* ws, int64_t m, int64_t d_out, int64_t d_in, int out, void* y, int64_t ldy,
+                  void* stream);
+int gptq_fp8_gated(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, const uint8_t* Wg,
+                   const float* gs, const uint8_t* Wu, const float* us, int64_t ldw, int64_t m, int64_t d_out,
+                   int64_t d_in, int act, int out, void* y, int64_t ldy, float* ys, int64_t ldys, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Token scores -- what a quantization cost, in the pages' own measure.
+ * Source: itwiki "GPTQ", "결과" (WikiText-2 perplexity before and after);
+ * blog "GPTQ를 밑바닥부터 구현하며 배운 것들", section 4 (loss and perplexity).
+ * Perplexity is exp of minus the mean log probability of the text's tokens.
+ *
+ * For every row i of logits, with p = softmax(logits[i]):
+ *   logp[i]     = ln p[targets[i]]; 0 for a negative target (a position that
+ *                 is not scored).  A target >= vocab is recorded as
+ *                 GPTQ_ERR_INVALID_ARG (detail: the row) and gives NaN.
+ *   entropy[i]  = - sum p ln p (may be NULL)
+ *   top_ids[i], top_logp[i]   the `top` largest p in descending order, equal
+ *                 ones by increasing index.
+ *   logits  device [n, vocab] of dtype (GPTQ_F32, GPTQ_BF16, GPTQ_F16), ld
+ *           elements between rows, ld >= vocab; aligned to the type's size.
+ *           -inf is a masked token: p = 0, logp = -inf.  A row of -inf alone
+ *           has logp = -inf, entropy 0 and the first `top` indices.  A NaN or
+ *           +inf is recorded as GPTQ_ERR_NONFINITE (detail: the row): the row's
+ *           results are NaN, its top_ids -1.
+ *   targets device int64 [n];  logp, entropy  device fp32 [n].
+ *   top     0 .. 32, at most vocab; top_logp fp32 and top_ids int32 [n, top],
+ *           both NULL for top = 0.
+ * 0 <= n <= 2^24, 1 <= vocab < 2^31.  fp32 arithmetic from the logits on; the
+ * same inputs give the same bits.  Overlaps as above.
+ * ---------------------------------------------------------------------- */
+int gptq_token_logprobs(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t ld,
+                        const int64_t* targets, float* logp, float* entropy, int top, float* top_logp,
+                        int32_t* top_ids, void* stream);
 
 /* ------------------------------------------------------------------------
  * Helpers on the same stream (not steps of the method).

@@ -40,6 +40,13 @@ SIGNATURES = {
     "gptq_dequant_gemv": (c_int, [c_vp, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_i64, c_vp, c_vp,
                                   c_size, c_vp]),
     "gptq_dequantize": (c_int, [c_vp, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_int, c_vp, c_vp]),
+    "gptq_fp8_quantize_rows": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "gptq_fp8_quantize_weight": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp]),
+    "gptq_fp8_gemm": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_i64,
+                              c_vp]),
+    "gptq_fp8_gated": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_int,
+                               c_int, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "gptq_token_logprobs": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_int, c_vp, c_vp, c_vp]),
     "gptq_widen_bf16": (c_int, [c_vp, c_vp, c_i64, c_vp]),
     "gptq_fill_f32": (c_int, [c_vp, c_i64, c_float, c_vp]),
     "gptq_get_status": (c_int, [c_vp, ctypes.POINTER(c_int)]),

@@ -251,6 +251,177 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, b
                                   _OUT_DTYPES[out.dtype], _ptr(out), _stream(stream)), "gptq_dequantize")
 
 
+# ----------------------------------------------------------------- 8-bit floating point
+_VALUE_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_CODE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+_FP8_OUT = 3
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _pitch(t, cols, name, step=1):
+    """Elements between the rows of a 2-D tensor with unit column stride (for
+    a single row any pitch will do: the next multiple of `step`)."""
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name} must have {cols} columns, got {tuple(t.shape)}")
+    rs, cs = t.stride()
+    if cs != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return rs if t.shape[0] > 1 else -(-cols // step) * step
+
+
+def _typed(t, dtypes, rows, name, device):
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {tuple(t.shape)}")
+
+
+_F32 = (torch.float32,)
+
+
+def _call(where, device, stream, *args):
+    """Call an entry point with `device` current and the stream last: the one
+    given, or the tensors' device's current one."""
+    fn = getattr(_lib(), where)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    if code:
+        raise GPTQError(code, where)
+
+
+def fp8_codes(rows: int, d_in: int, device="cuda") -> torch.Tensor:
+    """An uninitialized [rows, d_in] tensor of e4m3 codes whose row pitch is a
+    multiple of 16 bytes, as the calls below need it."""
+    return torch.empty((rows, -(-d_in // 16) * 16), dtype=torch.float8_e4m3fn, device=device)[:, :d_in]
+
+
+def fp8_blocks(n: int) -> int:
+    """Scale blocks along `n` values."""
+    return -(-n // 128)
+
+
+def fp8_quantize_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """e4m3 codes of activations x [m, d_in] (fp32, bf16 or fp16; rows may be
+    pitched) with a scale per token and 128 channels: codes [m, d_in] (float8_e4m3fn
+    or uint8, 16-byte row pitch), scales [fp8_blocks(d_in), m] fp32."""
+    m, d = x.shape
+    dev = x.device
+    _typed(x, _VALUE_DTYPES, m, "x", dev)
+    _typed(codes, _CODE_DTYPES, m, "codes", dev)
+    _typed(scales, _F32, fp8_blocks(d), "scales", dev)
+    _call("gptq_fp8_quantize_rows", dev, stream, x.data_ptr(), _VALUE_DTYPES[x.dtype], m, d, _pitch(x, d, "x"),
+          codes.data_ptr(), _pitch(codes, d, "codes", 16), scales.data_ptr(), _pitch(scales, m, "scales"))
+
+
+def fp8_quantize_weight(W: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """e4m3 codes of a weight W [d_out, d_in] with a scale per 128 x 128 block:
+    codes [d_out, d_in], scales [fp8_blocks(d_out), fp8_blocks(d_in)] fp32."""
+    n, d = W.shape
+    dev = W.device
+    _typed(W, _VALUE_DTYPES, n, "W", dev)
+    _typed(codes, _CODE_DTYPES, n, "codes", dev)
+    _weight_scales(scales, n, d, "scales", dev)
+    _call("gptq_fp8_quantize_weight", dev, stream, W.data_ptr(), _VALUE_DTYPES[W.dtype], n, d, _pitch(W, d, "W"),
+          codes.data_ptr(), _pitch(codes, d, "codes", 16), scales.data_ptr())
+
+
+def _weight_scales(scales, n, d, name, dev):
+    _typed(scales, _F32, fp8_blocks(n), name, dev)
+    if scales.shape[1] != fp8_blocks(d) or not scales.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{fp8_blocks(n)}, {fp8_blocks(d)}]")
+
+
+def _fp8_operands(x, x_scales, w, w_scales, y):
+    m, d = x.shape
+    n = w.shape[0]
+    dev = x.device
+    _typed(x, _CODE_DTYPES, m, "x", dev)
+    _typed(x_scales, _F32, fp8_blocks(d), "x_scales", dev)
+    _typed(w, _CODE_DTYPES, n, "w", dev)
+    _weight_scales(w_scales, n, d, "w_scales", dev)
+    return m, n, d, dev
+
+
+def fp8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, y: torch.Tensor,
+             stream=None):
+    """y = x w^T from codes and scales (as the two calls above write them), y
+    [m, d_out] fp32, bf16 or fp16; rows may be pitched."""
+    m, n, d, dev = _fp8_operands(x, x_scales, w, w_scales, y)
+    _typed(y, _VALUE_DTYPES, m, "y", dev)
+    _call("gptq_fp8_gemm", dev, stream, x.data_ptr(), _pitch(x, d, "x", 16), x_scales.data_ptr(),
+          _pitch(x_scales, m, "x_scales"), w.data_ptr(), _pitch(w, d, "w", 16), w_scales.data_ptr(), m, n, d,
+          _VALUE_DTYPES[y.dtype], y.data_ptr(), _pitch(y, n, "y"))
+
+
+def fp8_gated(x: torch.Tensor, x_scales: torch.Tensor, gate: torch.Tensor, gate_scales: torch.Tensor,
+              up: torch.Tensor, up_scales: torch.Tensor, y: torch.Tensor, y_scales: torch.Tensor | None = None,
+              act: str = "silu", stream=None):
+    """y = act(x gate^T) * (x up^T) in one kernel, act "silu" or "gelu": values
+    (y fp32, bf16 or fp16), or codes (y float8_e4m3fn or uint8) with y_scales
+    [fp8_blocks(d_out), m], ready for the next product."""
+    m, n, d, dev = _fp8_operands(x, x_scales, gate, gate_scales, y)
+    _typed(up, _CODE_DTYPES, n, "up", dev)
+    _weight_scales(up_scales, n, d, "up_scales", dev)
+    ldw = _pitch(gate, d, "gate", 16)
+    if _pitch(up, d, "up", 16) != ldw:
+        raise ValueError("gate and up must have the same row pitch")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if y.dtype in _CODE_DTYPES:
+        _typed(y, _CODE_DTYPES, m, "y", dev)
+        if y_scales is None:
+            raise ValueError("codes need y_scales")
+        _typed(y_scales, _F32, fp8_blocks(n), "y_scales", dev)
+        out, ldy, ys, ldys = _FP8_OUT, _pitch(y, n, "y", 16), y_scales.data_ptr(), _pitch(y_scales, m, "y_scales")
+    else:
+        _typed(y, _VALUE_DTYPES, m, "y", dev)
+        if y_scales is not None:
+            raise ValueError("y_scales go with codes only")
+        out, ldy, ys, ldys = _VALUE_DTYPES[y.dtype], _pitch(y, n, "y"), None, 0
+    _call("gptq_fp8_gated", dev, stream, x.data_ptr(), _pitch(x, d, "x", 16), x_scales.data_ptr(),
+          _pitch(x_scales, m, "x_scales"), gate.data_ptr(), gate_scales.data_ptr(), up.data_ptr(),
+          up_scales.data_ptr(), ldw, m, n, d, _ACTS[act], out, y.data_ptr(), ldy, ys, ldys)
+
+
+# ----------------------------------------------------------------- token scores
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, logp: torch.Tensor,
+                   entropy: torch.Tensor | None = None, top_logp: torch.Tensor | None = None,
+                   top_ids: torch.Tensor | None = None, stream=None):
+    """Per row of logits [n, vocab] (fp32, bf16 or fp16; rows may be pitched):
+    logp[i] = ln softmax(logits[i])[targets[i]] (0 where targets[i] < 0), the
+    entropy, and, with top_logp and top_ids [n, k], the k <= 32 likeliest
+    tokens (equal ones by increasing index).  targets int64."""
+    n, v = logits.shape
+    dev = logits.device
+    _typed(logits, _VALUE_DTYPES, n, "logits", dev)
+    _vector(targets, torch.int64, n, "targets", dev)
+    _vector(logp, torch.float32, n, "logp", dev)
+    if entropy is not None:
+        _vector(entropy, torch.float32, n, "entropy", dev)
+    if (top_logp is None) != (top_ids is None):
+        raise ValueError("top_logp and top_ids go together")
+    k = 0
+    if top_logp is not None:
+        k = top_logp.shape[-1]
+        for t, dtype, name in ((top_logp, torch.float32, "top_logp"), (top_ids, torch.int32, "top_ids")):
+            if t.device != dev or t.dtype != dtype or t.shape != (n, k) or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dtype} [{n}, {k}] on the logits' device")
+    _call("gptq_token_logprobs", dev, stream, logits.data_ptr(), _VALUE_DTYPES[logits.dtype], n, v,
+          _pitch(logits, v, "logits"), targets.data_ptr(), logp.data_ptr(),
+          None if entropy is None else entropy.data_ptr(), k, top_logp.data_ptr() if k else None,
+          top_ids.data_ptr() if k else None)
+
+
+def _vector(t, dtype, n, name, dev):
+    if t.device != dev or t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} [{n}] on the logits' device")
+
+
 def widen_bf16(src: torch.Tensor, dst: torch.Tensor, stream=None):
     if src.dtype != torch.bfloat16 or dst.dtype != torch.float32 or src.numel() != dst.numel():
         raise ValueError("widen_bf16: bf16 -> fp32 of equal size")

@@ -61,6 +61,61 @@ inline bool valid_d_in(int64_t d_in) { return d_in >= 128 && d_in <= 32768 && d_
 inline bool valid_bits(int bits) { return bits == 2 || bits == 3 || bits == 4 || bits == 8; }
 inline bool valid_group(int g, int64_t d_in) { return g == -1 || (g > 0 && g % 128 == 0 && d_in % g == 0); }
 
+// ---- the 8-bit floating-point form and the token scores
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+inline bool valid_value_dtype(int t) { return t == GPTQ_F32 || t == GPTQ_BF16 || t == GPTQ_F16; }
+inline int64_t value_bytes(int t) { return t == GPTQ_F32 ? 4 : t == GPTQ_FP8 ? 1 : 2; }
+inline bool valid_values(const void* p, int t) {
+    return p && (reinterpret_cast<uintptr_t>(p) & uintptr_t(value_bytes(t) - 1)) == 0;
+}
+inline bool valid_f32(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool valid_fp8_d_in(int64_t d) { return d >= 1 && d <= (int64_t(1) << 18); }
+inline bool valid_fp8_d_out(int64_t n) { return n >= 1 && n <= (int64_t(1) << 22); }
+constexpr int64_t kMaxLd = int64_t(1) << 36;   // rows * pitch stays inside 64 bits
+inline bool valid_ld(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; }
+inline bool valid_codes(const void* p, int64_t d, int64_t ld) {
+    return p && aligned16(p) && valid_ld(ld, d) && ld % 16 == 0;
+}
+inline int64_t fp8_blocks(int64_t d) { return (d + 127) / 128; }
+
+// The bytes from the first to the last element of `rows` rows of `cols`
+// elements, `ld` elements apart.  (Rows of two pitched arrays may interleave
+// without sharing an element; such spans count as overlapping.)
+struct Span {
+    uintptr_t lo, hi;
+};
+inline Span pitched(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, rows <= 0 ? lo : lo + uintptr_t(((rows - 1) * ld + cols) * bytes)};
+}
+inline bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+
+int fp8_product(const Fp8Product& p, void* stream) {
+    if (p.m < 0 || p.m > kMaxTokens || !valid_fp8_d_out(p.n) || !valid_fp8_d_in(p.d)) return GPTQ_ERR_INVALID_ARG;
+    if (p.m == 0) return GPTQ_OK;
+    if (!valid_codes(p.x, p.d, p.ldx) || !valid_f32(p.xs) || !valid_ld(p.lds, p.m) ||
+        !valid_codes(p.w, p.d, p.ldw) || !valid_f32(p.ws))
+        return GPTQ_ERR_INVALID_ARG;
+    if (p.u && (!valid_codes(p.u, p.d, p.ldu) || !valid_f32(p.us))) return GPTQ_ERR_INVALID_ARG;
+    if (p.out == GPTQ_FP8 ? (!valid_codes(p.y, p.n, p.ldy) || !valid_f32(p.ys) || !valid_ld(p.ldys, p.m))
+                          : (!valid_values(p.y, p.out) || !valid_ld(p.ldy, p.n) || p.ys))
+        return GPTQ_ERR_INVALID_ARG;
+    const int64_t nb = fp8_blocks(p.d);
+    const Span in[6] = {pitched(p.x, p.m, p.d, p.ldx, 1),  pitched(p.xs, nb, p.m, p.lds, 4),
+                        pitched(p.w, p.n, p.d, p.ldw, 1),  pitched(p.ws, fp8_blocks(p.n), nb, nb, 4),
+                        pitched(p.u, p.u ? p.n : 0, p.d, p.ldu, 1),
+                        pitched(p.us, p.u ? fp8_blocks(p.n) : 0, nb, nb, 4)};
+    const Span y = pitched(p.y, p.m, p.n, p.ldy, value_bytes(p.out));
+    const Span ys = pitched(p.ys, p.ys ? fp8_blocks(p.n) : 0, p.m, p.ldys, 4);
+    if (overlap(y, ys)) return GPTQ_ERR_INVALID_ARG;
+    for (const Span& s : in)
+        if (overlap(y, s) || overlap(ys, s)) return GPTQ_ERR_INVALID_ARG;
+    DevStatus* st = nullptr;
+    PFN_encodeTiled enc = nullptr;
+    if (status_ptr(&st) || encode_fn(&enc)) return GPTQ_ERR_CUDA;
+    return launch_fp8_product(p, static_cast<cudaStream_t>(stream), st, enc);
+}
+
 }  // namespace
 
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
@@ -277,6 +332,81 @@ int gptq_dequantize(const uint32_t* codes, const uint16_t* scales, const uint16_
     if (status_ptr(&st)) return GPTQ_ERR_CUDA;
     return launch_dequantize(codes, scales, zeros, d_out, d_in, bits, groupsize, perm, out_dtype, out,
                              static_cast<cudaStream_t>(stream), st);
+}
+
+int gptq_fp8_quantize_rows(const void* x, int dtype, int64_t m, int64_t d_in, int64_t ldx, uint8_t* codes,
+                           int64_t ldc, float* scales, int64_t lds, void* stream) {
+    if (!valid_value_dtype(dtype) || m < 0 || m > kMaxTokens || !valid_fp8_d_in(d_in)) return GPTQ_ERR_INVALID_ARG;
+    if (m == 0) return GPTQ_OK;
+    if (!valid_values(x, dtype) || !valid_ld(ldx, d_in) || !valid_codes(codes, d_in, ldc) || !valid_f32(scales) ||
+        !valid_ld(lds, m))
+        return GPTQ_ERR_INVALID_ARG;
+    const Span in = pitched(x, m, d_in, ldx, value_bytes(dtype));
+    const Span c = pitched(codes, m, d_in, ldc, 1), s = pitched(scales, fp8_blocks(d_in), m, lds, 4);
+    if (overlap(c, in) || overlap(s, in) || overlap(c, s)) return GPTQ_ERR_INVALID_ARG;
+    DevStatus* st = nullptr;
+    if (status_ptr(&st)) return GPTQ_ERR_CUDA;
+    return launch_fp8_quantize_rows(x, dtype, m, d_in, ldx, codes, ldc, scales, lds,
+                                    static_cast<cudaStream_t>(stream), st);
+}
+
+int gptq_fp8_quantize_weight(const void* W, int dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* codes,
+                             int64_t ldc, float* scales, void* stream) {
+    if (!valid_value_dtype(dtype) || !valid_fp8_d_out(d_out) || !valid_fp8_d_in(d_in)) return GPTQ_ERR_INVALID_ARG;
+    if (!valid_values(W, dtype) || !valid_ld(ldw, d_in) || !valid_codes(codes, d_in, ldc) || !valid_f32(scales))
+        return GPTQ_ERR_INVALID_ARG;
+    const int64_t nb = fp8_blocks(d_in);
+    const Span in = pitched(W, d_out, d_in, ldw, value_bytes(dtype));
+    const Span c = pitched(codes, d_out, d_in, ldc, 1), s = pitched(scales, fp8_blocks(d_out), nb, nb, 4);
+    if (overlap(c, in) || overlap(s, in) || overlap(c, s)) return GPTQ_ERR_INVALID_ARG;
+    DevStatus* st = nullptr;
+    if (status_ptr(&st)) return GPTQ_ERR_CUDA;
+    return launch_fp8_quantize_weight(W, dtype, d_out, d_in, ldw, codes, ldc, scales,
+                                      static_cast<cudaStream_t>(stream), st);
+}
+
+int gptq_fp8_gemm(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, const uint8_t* w, int64_t ldw,
+                  const float* ws, int64_t m, int64_t d_out, int64_t d_in, int out, void* y, int64_t ldy,
+                  void* stream) {
+    if (!valid_value_dtype(out)) return GPTQ_ERR_INVALID_ARG;
+    const Fp8Product p{x, xs, w, ws, nullptr, nullptr, y, nullptr, m, d_out, d_in, ldx, lds, ldw, ldw, ldy, 0, out, 0};
+    return fp8_product(p, stream);
+}
+
+int gptq_fp8_gated(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, const uint8_t* Wg, const float* gs,
+                   const uint8_t* Wu, const float* us, int64_t ldw, int64_t m, int64_t d_out, int64_t d_in, int act,
+                   int out, void* y, int64_t ldy, float* ys, int64_t ldys, void* stream) {
+    if (!valid_value_dtype(out) && out != GPTQ_FP8) return GPTQ_ERR_INVALID_ARG;
+    if (act != 0 && act != 1) return GPTQ_ERR_INVALID_ARG;
+    if (m != 0 && (!Wu || !us)) return GPTQ_ERR_INVALID_ARG;   // a null second weight is the plain product below
+    const Fp8Product p{x, xs, Wg, gs, Wu, us, y, ys, m, d_out, d_in, ldx, lds, ldw, ldw, ldy, ldys, out, act};
+    return fp8_product(p, stream);
+}
+
+int gptq_token_logprobs(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t ld, const int64_t* targets,
+                        float* logp, float* entropy, int top, float* top_logp, int32_t* top_ids, void* stream) {
+    if (!valid_value_dtype(dtype) || n < 0 || n > kMaxTokens || vocab < 1 || vocab >= (int64_t(1) << 31) ||
+        !valid_ld(ld, vocab) || top < 0 || top > 32 || top > vocab)
+        return GPTQ_ERR_INVALID_ARG;
+    if (n == 0) return GPTQ_OK;
+    if (!valid_values(logits, dtype) || !targets || (reinterpret_cast<uintptr_t>(targets) & 7u) || !valid_f32(logp) ||
+        (reinterpret_cast<uintptr_t>(entropy) & 3u))
+        return GPTQ_ERR_INVALID_ARG;
+    if (top == 0 ? (top_logp || top_ids)
+                 : (!valid_f32(top_logp) || !top_ids || (reinterpret_cast<uintptr_t>(top_ids) & 3u)))
+        return GPTQ_ERR_INVALID_ARG;
+    const Span in = pitched(logits, n, vocab, ld, value_bytes(dtype)), tg = pitched(targets, 1, n, n, 8);
+    const Span outs[4] = {pitched(logp, 1, n, n, 4), pitched(entropy, entropy ? 1 : 0, n, n, 4),
+                          pitched(top_logp, top ? n : 0, top, top, 4), pitched(top_ids, top ? n : 0, top, top, 4)};
+    for (int i = 0; i < 4; ++i) {
+        if (overlap(outs[i], in) || overlap(outs[i], tg)) return GPTQ_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return GPTQ_ERR_INVALID_ARG;
+    }
+    DevStatus* st = nullptr;
+    if (status_ptr(&st)) return GPTQ_ERR_CUDA;
+    return launch_token_logprobs(logits, dtype, n, vocab, ld, targets, logp, entropy, top, top_logp, top_ids,
+                                 static_cast<cudaStream_t>(stream), st);
 }
 
 int gptq_widen_bf16(const uint16_t* src, float* dst, int64_t count, void* stream) {

@@ -1,0 +1,403 @@
+// Products of e4m3 codes with one fp32 scale per block of 128, on the tcgen05
+// tensor cores (kind::f8f6f4).
+//
+//   y[t][r] = sum_b sx[b][t] sw[r / 128][b] sum_{k in block b} xc[t][k] wc[r][k]
+//
+// The scales change every 128 values of k, so they cannot wait for the
+// epilogue: the MMAs of one block of k (four of K = 32, one 128-byte swizzle
+// row of codes) fill a TMEM accumulator of their own, and four warps then read
+// it and add it, times the block's scales, to the tile's sums in fp32 registers.
+// A ring of accumulators keeps the tensor cores running meanwhile.  Sums inside
+// a block are the tensor core's fp32 accumulation; products of two e4m3
+// values are exact there.
+//
+// The gated pair runs both products of the same tokens in one kernel, so the
+// tokens' codes are read once and neither product is written out:
+//   h[t][r] = act(g[t][r]) u[t][r]
+// as values, or as the e4m3 codes and scales that the next product takes (a
+// tile holds 128 features of a token, exactly one of that product's blocks).
+#include <atomic>
+#include <cstring>
+
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace gptq {
+namespace fp8 {
+
+constexpr int TILE_BYTES = 128 * 128;   // 128 rows of one 128-byte block of k
+constexpr int OUT_CODES = 3;            // Args::out beside the gptq_dtype values
+
+struct Maps {
+    CUtensorMap w, u, x;   // weight, second weight (gated), tokens
+};
+
+struct Args {
+    int64_t m, n, lds, ldy, ldys;
+    const float *xs, *ws, *us;
+    void* y;
+    float* ys;
+    int nkb, out, act;
+    DevStatus* st;
+};
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4: e4m3 x e4m3 -> f32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// 32 lanes x 16 columns without waiting; tmem_ld_done() before the values are used.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Wait for this thread's TMEM loads; the values pass through it so that no
+// use of them can be moved in front of the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// act(g): 0 silu, g / (1 + e^-g); 1 gelu in its exact form, g Phi(g), with Phi
+// from erfc so that large negative gates keep their relative accuracy.
+__device__ __forceinline__ float gate_act(float g, int act) {
+    if (act == 0) return g / (1.0f + expf(-g));
+    return 0.5f * g * erfcf(g * -0.70710678118654752f);
+}
+
+__device__ __forceinline__ void store_out(void* y, int64_t at, float v, int out) {
+    if (out == GPTQ_F32)
+        static_cast<float*>(y)[at] = v;
+    else if (out == GPTQ_BF16)
+        static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(y)[at] = __float2half_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// Weights on the MMA's M side: a tile is 128 weight rows (one row of scale
+// blocks) by NT tokens, which keeps the tile full for one token as for 128.
+// The cluster's CTAs share a tile's blocks of k and add their sums through
+// distributed shared memory in rank order: no workspace, no atomics, the same
+// bits on every call.
+template <int NT, bool GATED>
+struct Narrow {
+    static constexpr int ACC = GATED ? 2 : 1;
+    static constexpr int STAGE_BYTES = ACC * TILE_BYTES + NT * 128;
+    static constexpr int STAGES = GATED ? 3 : 4;
+    static constexpr int SLOTS = 4;                      // TMEM accumulators
+    static constexpr int COLS = SLOTS * ACC * NT;        // a power of two, 64 .. 512
+    static constexpr int THREADS = 192;                  // 4 warps of sums, 1 of loads, 1 of MMAs
+    static constexpr int RING = 2 * ACC * NT;            // floats of scales per warp
+    static constexpr size_t SMEM_BYTES =
+        1024 + size_t(STAGES) * STAGE_BYTES + (4 * RING + 4 * NT) * 4 + (2 * STAGES + 2 * SLOTS) * 8 + 16;
+    // the sums that the cluster exchanges, and the gated values, reuse the stages
+    static_assert((ACC * NT + (GATED ? NT : 0)) * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
+    static_assert(SMEM_BYTES <= 232448, "shared memory");
+    static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0, "TMEM columns");
+};
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
+    narrow_kernel(const __grid_constant__ Maps maps, const Args g) {
+    using C = Narrow<NT, GATED>;
+    constexpr int ACC = C::ACC;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* ring_all = reinterpret_cast<float*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);   // [4][2][ACC * NT]
+    uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + 4 * C::RING);                    // [NT][4]
+    uint64_t* full = reinterpret_cast<uint64_t*>(amax + 4 * NT);   // [STAGES] TMA landed
+    uint64_t* empty = full + C::STAGES;                            // [STAGES] MMAs done with the stage
+    uint64_t* tfull = empty + C::STAGES;                           // [SLOTS] accumulator complete
+    uint64_t* tempty = tfull + C::SLOTS;                           // [SLOTS] accumulator read by four warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + C::SLOTS);
+
+    uint32_t split;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    const uint32_t rank = cluster_ctarank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = int(blockIdx.x / split);
+    const int64_t row0 = int64_t(tile) * 128, tok0 = int64_t(blockIdx.y) * NT;
+    const int b0 = int(int64_t(g.nkb) * rank / split), b1 = int(int64_t(g.nkb) * (rank + 1) / split);
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&maps.w);
+        if (GATED) tma_prefetch_desc(&maps.u);
+        tma_prefetch_desc(&maps.x);
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < C::SLOTS; ++s) {
+            mbar_init(&tfull[s], 1);
+            mbar_init(&tempty[s], 4);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, C::COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    float acc[ACC * NT];
+#pragma unroll
+    for (int c = 0; c < ACC * NT; ++c) acc[c] = 0.0f;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            for (int b = b0; b < b1; ++b) {
+                const int i = b - b0, s = i % C::STAGES;
+                if (!mbar_wait(&empty[s], (uint32_t(i / C::STAGES) & 1u) ^ 1u, g.st, 401)) break;
+                uint8_t* base = smem + size_t(s) * C::STAGE_BYTES;
+                mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+                tma_load_2d(base, &maps.w, b * 128, int(row0), &full[s]);
+                if (GATED) tma_load_2d(base + TILE_BYTES, &maps.u, b * 128, int(row0), &full[s]);
+                tma_load_2d(base + ACC * TILE_BYTES, &maps.x, b * 128, int(tok0), &full[s]);
+            }
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(128, NT);
+            for (int b = b0; b < b1; ++b) {
+                const int i = b - b0, s = i % C::STAGES, d = i % C::SLOTS;
+                if (!mbar_wait(&tempty[d], (uint32_t(i / C::SLOTS) & 1u) ^ 1u, g.st, 402)) break;
+                if (!mbar_wait(&full[s], uint32_t(i / C::STAGES) & 1u, g.st, 403)) break;
+                tc_fence_after();
+                const uint32_t wa = smem_u32(smem + size_t(s) * C::STAGE_BYTES), xa = wa + ACC * TILE_BYTES;
+                const uint32_t dt = tmem_base + uint32_t(d * ACC * NT);
+#pragma unroll
+                for (int a = 0; a < ACC; ++a)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // 32 codes (32 bytes) of the 128-byte swizzle row
+                        umma_f8(dt + a * NT, sdesc_sw128(wa + a * TILE_BYTES + kk * 32, 16, 1024),
+                                sdesc_sw128(xa + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+                umma_commit(&empty[s]);
+                umma_commit(&tfull[d]);
+            }
+        }
+    } else {
+        // ---------------- sums: thread = weight row (TMEM lane), registers = tokens
+        float* ring = ring_all + warp * C::RING;
+        constexpr int PER = (NT + 31) / 32;
+        float sx[PER], sw[ACC];
+        auto fetch = [&](int b) {
+#pragma unroll
+            for (int p = 0; p < PER; ++p) {
+                const int64_t t = tok0 + lane + 32 * p;
+                sx[p] = lane + 32 * p < NT && t < g.m ? __ldg(g.xs + int64_t(b) * g.lds + t) : 0.0f;
+            }
+            sw[0] = __ldg(g.ws + int64_t(tile) * g.nkb + b);
+            if (GATED) sw[ACC - 1] = __ldg(g.us + int64_t(tile) * g.nkb + b);
+        };
+        fetch(b0);
+        for (int b = b0; b < b1; ++b) {
+            const int i = b - b0, d = i % C::SLOTS;
+            float* mine = ring + (i & 1) * ACC * NT;
+#pragma unroll
+            for (int a = 0; a < ACC; ++a)
+#pragma unroll
+                for (int p = 0; p < PER; ++p)
+                    if (lane + 32 * p < NT) mine[a * NT + lane + 32 * p] = sx[p] * sw[a];
+            __syncwarp();
+            if (b + 1 < b1) fetch(b + 1);
+            const bool ok = mbar_wait(&tfull[d], uint32_t(i / C::SLOTS) & 1u, g.st, 404);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const uint32_t dt = tmem_base + (uint32_t(warp * 32) << 16) + uint32_t(d * ACC * NT);
+#pragma unroll
+            for (int j = 0; j < ACC * NT; j += 16) {
+                uint32_t v[16];
+                tmem_ld_x16(dt + j, v);
+                tmem_ld_done(v);
+                if (j + 16 == ACC * NT) {   // this warp has read the whole accumulator
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[d]);
+                }
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    const float4 s = *reinterpret_cast<const float4*>(mine + j + q);
+                    acc[j + q] = fmaf(__uint_as_float(v[q]), s.x, acc[j + q]);
+                    acc[j + q + 1] = fmaf(__uint_as_float(v[q + 1]), s.y, acc[j + q + 1]);
+                    acc[j + q + 2] = fmaf(__uint_as_float(v[q + 2]), s.z, acc[j + q + 2]);
+                    acc[j + q + 3] = fmaf(__uint_as_float(v[q + 3]), s.w, acc[j + q + 3]);
+                }
+            }
+        }
+    }
+    // The accumulators are in registers: TMEM goes back before this CTA waits
+    // for others, so a CTA that holds TMEM never depends on one that waits for it.
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem_base, C::COLS);
+
+    float* part = reinterpret_cast<float*>(smem);   // [ACC * NT][128] this CTA's sums
+    if (warp < 4) {
+#pragma unroll
+        for (int c = 0; c < ACC * NT; ++c) part[c * 128 + threadIdx.x] = acc[c];
+    }
+    __syncwarp();
+    cluster_sync();
+    const int cols = int(min(int64_t(NT), g.m - tok0));
+    if (warp < 4) {
+        const int r = threadIdx.x;
+        const int64_t row = row0 + r;
+        float* held = part + ACC * NT * 128;        // gated values until their block's scale is known
+        for (int c = int(rank); c < cols; c += int(split)) {
+            float v = 0.0f, u = 0.0f;
+            for (uint32_t q = 0; q < split; ++q) {
+                v += ld_cluster_f32(mapa_shared(part + c * 128 + r, q));
+                if (GATED) u += ld_cluster_f32(mapa_shared(part + (NT + c) * 128 + r, q));
+            }
+            if (GATED) v = gate_act(v, g.act) * u;
+            if (GATED && g.out == OUT_CODES) {
+                held[c * 128 + r] = v;
+                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
+                if (lane == 0) amax[c * 4 + warp] = top;
+            } else if (row < g.n) {
+                store_out(g.y, (tok0 + c) * g.ldy + row, v, g.out);
+            }
+        }
+        if (GATED && g.out == OUT_CODES) {
+            named_barrier_sync(1, 128);
+            for (int c = int(rank); c < cols; c += int(split)) {
+                const uint32_t a = max(max(amax[4 * c], amax[4 * c + 1]), max(amax[4 * c + 2], amax[4 * c + 3]));
+                float s = block_scale(a), v = held[c * 128 + r];
+                if (r == 0) {
+                    g.ys[int64_t(tile) * g.ldys + tok0 + c] = s;
+                    if (a >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, int(tok0 + c));
+                }
+                if (s < SMALL_SCALE) {
+                    s *= SMALL_LIFT;
+                    v *= SMALL_LIFT;
+                }
+                if (row < g.n)
+                    static_cast<uint8_t*>(g.y)[(tok0 + c) * g.ldy + row] =
+                        uint8_t(e4m3x2(quotient(v, s, __frcp_rn(s)), 0.0f));
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // peers have read this CTA's sums
+}
+
+}  // namespace fp8
+
+namespace {
+
+constexpr int kMaxDev = 64;
+
+// Codes [rows, d] with row pitch ld bytes, 128-byte swizzled boxes of box_rows rows.
+int make_code_map(PFN_encodeTiled encode, CUtensorMap* tm, const uint8_t* base, int64_t rows, int64_t d, int64_t ld,
+                  uint32_t box_rows) {
+    const cuuint64_t dims[2] = {cuuint64_t(d), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld)};
+    const cuuint32_t box[2] = {128, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box,
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GPTQ_OK : GPTQ_ERR_CUDA;
+}
+
+int sm_count(int dev, int* out) {
+    static std::atomic<int> sms[kMaxDev];
+    if (dev < 0 || dev >= kMaxDev) return GPTQ_ERR_CUDA;
+    int n = sms[dev].load();
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return GPTQ_ERR_CUDA;
+        sms[dev].store(n);
+    }
+    *out = n;
+    return GPTQ_OK;
+}
+
+template <int NT, bool GATED>
+int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
+    using C = fp8::Narrow<NT, GATED>;
+    auto kernel = fp8::narrow_kernel<NT, GATED>;
+    static std::atomic<int> per_sm[kMaxDev];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || sm_count(dev, &sms)) return GPTQ_ERR_CUDA;
+    if (per_sm[dev].load() == 0) {
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM_BYTES)) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, C::THREADS, C::SMEM_BYTES) != cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        per_sm[dev].store(std::max(1, n));
+    }
+    fp8::Maps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    int rc = make_code_map(encode, &maps.w, p.w, p.n, p.d, p.ldw, 128);
+    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, 128);
+    if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, NT);
+    if (rc) return rc;
+    fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, p.act, st};
+    // As many CTAs per tile as fill the GPU once, up to a portable cluster.
+    const int64_t rows = (p.n + 127) / 128, toks = (p.m + NT - 1) / NT;
+    const int64_t split = std::max<int64_t>(
+        1, std::min<int64_t>(std::min<int64_t>(8, g.nkb), int64_t(sms) * per_sm[dev].load() / (rows * toks)));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(rows * split), unsigned(toks));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, maps, g) != cudaSuccess) return GPTQ_ERR_CUDA;
+    count_launch();
+    return GPTQ_OK;
+}
+
+}  // namespace
+
+int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
+    if (p.u) {
+        if (p.m <= 16) return launch_narrow<16, true>(p, stream, st, encode);
+        if (p.m <= 32) return launch_narrow<32, true>(p, stream, st, encode);
+        return launch_narrow<64, true>(p, stream, st, encode);
+    }
+    if (p.m <= 16) return launch_narrow<16, false>(p, stream, st, encode);
+    if (p.m <= 32) return launch_narrow<32, false>(p, stream, st, encode);
+    if (p.m <= 64) return launch_narrow<64, false>(p, stream, st, encode);
+    return launch_narrow<128, false>(p, stream, st, encode);
+}
+
+}  // namespace gptq

@@ -77,6 +77,37 @@ int launch_dequantize(const uint32_t* codes, const uint16_t* scales, const uint1
                       int64_t d_in, int bits, int groupsize, const int32_t* perm, int out_dtype, void* out,
                       cudaStream_t stream, DevStatus* st);
 
+// fp8_quant.cu: e4m3 codes and fp32 scales of 1 x 128 blocks (scales
+// [blocks, m], row pitch lds) or of 128 x 128 blocks (scales [row blocks,
+// blocks], dense).  ldx, ldw count elements, ldc bytes (a multiple of 16).
+int launch_fp8_quantize_rows(const void* x, int dtype, int64_t m, int64_t d, int64_t ldx, uint8_t* codes,
+                             int64_t ldc, float* scales, int64_t lds, cudaStream_t stream, DevStatus* st);
+int launch_fp8_quantize_weight(const void* w, int dtype, int64_t n, int64_t d, int64_t ldw, uint8_t* codes,
+                               int64_t ldc, float* scales, cudaStream_t stream, DevStatus* st);
+
+// fp8_gemm.cu: y = x w^T from codes and scales, or with a second weight u the
+// gated pair act(x w^T) * (x u^T).  out: a gptq_dtype, or 3 for codes (y)
+// and scales (ys [blocks, m], row pitch ldys), gated only.
+struct Fp8Product {
+    const uint8_t* x;
+    const float* xs;
+    const uint8_t* w;
+    const float* ws;
+    const uint8_t* u;
+    const float* us;
+    void* y;
+    float* ys;
+    int64_t m, n, d, ldx, lds, ldw, ldu, ldy, ldys;
+    int out, act;
+};
+int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode);
+
+// logprobs.cu: per row of logits the target's log probability, the entropy
+// (may be null) and the `top` (0 .. 32) likeliest tokens.
+int launch_token_logprobs(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t ld,
+                          const int64_t* targets, float* logp, float* entropy, int top, float* top_logp,
+                          int32_t* top_ids, cudaStream_t stream, DevStatus* st);
+
 // permute.cu (act-order): the processing order from diag(H), the permuted
 // Hessian, and the column permutation of a row-major matrix (in place allowed).
 int launch_act_order_perm(const float* H, int64_t d, int32_t* perm, cudaStream_t stream);
