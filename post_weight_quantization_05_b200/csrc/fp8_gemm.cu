@@ -310,6 +310,315 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     cluster_sync();   // peers have read this CTA's sums
 }
 
+// ---------------------------------------------------------------------------
+// Tokens on the MMA's M side, for prompts: a cluster of two CTAs owns a tile of
+// 256 tokens by 256 weight rows (gated: 128 rows of each weight) and runs it as
+// cta_group::2 MMAs (M = N = 256, K = 32).  CTA r loads tokens 128 r .. 128 r +
+// 127 of the tile and its half of the weight rows (gated: r = 0 the gate's,
+// r = 1 the up projection's), 32 KB per block of k, and holds its tokens' 256
+// sums: one block fills 256 TMEM columns in 512 clocks, and two accumulators
+// take turns.  Eight warps keep the sums, a token per lane and 128 columns per
+// thread, so a block's scales are one number per thread (gated: two).  One CTA
+// alone would load 48 KB a block for the same MMA work, past the 128 bytes per
+// clock that shared memory gives at the tensor cores' e4m3 rate.
+struct Wide {
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int STAGES = 6;
+    static constexpr int SLOTS = 2;
+    static constexpr int SUM_WARPS = 8;
+    static constexpr int THREADS = 32 * (SUM_WARPS + 4);  // and a warp each for loads and MMAs, two idle
+    // Registers per thread after the split between the sums' two warpgroups and
+    // the third; the launch checks that they fit what it was given.
+    static constexpr int SUM_REGS = 216, OTHER_REGS = 72;
+    static constexpr int AHEAD = 4;                       // blocks of scales in flight per thread
+    static constexpr int RING = 8;                        // blocks of scales per warp
+    static constexpr int SCALES = 3;                      // token, weight, second weight
+    static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * RING * SCALES * 32 * 4 +
+                                         2 * 2 * 128 * 4 + (2 * STAGES + 2 * SLOTS) * 8 + 16;
+    static_assert(SMEM_BYTES <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Arrive on an mbarrier of either CTA without publishing memory: for an
+// accumulator that has been read (its loads have returned) nothing else needs
+// to be ordered, and a release at cluster scope would wait for every copy and
+// store this thread has in flight (measured: it was the kernel's whole time,
+// 1.9 ms instead of 0.7 at 4096 x 8192 x 28672).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// 4-byte asynchronous copy to shared memory; zero if !live (src is not read).
+__device__ __forceinline__ void copy4_async(float* dst, const float* src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 4 : 0)
+                 : "memory");
+}
+
+// Tile t of tiles_m x tiles_n, in groups of eight tile rows: the tiles that run
+// at the same time share few token and weight rows, which L2 then serves.
+__device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm,
+                                             uint32_t& tn) {
+    constexpr uint32_t G = 8;
+    const uint32_t group = t / (G * tiles_n), in = t % (G * tiles_n);
+    const uint32_t rows = min(G, tiles_m - group * G);
+    tm = group * G + in % rows;
+    tn = in / rows;
+}
+
+// COLS consecutive values of one output row; `vec`: 16-byte stores are aligned.
+template <typename T, int COLS>
+__device__ __forceinline__ void store_row(T* y, const float* v, int64_t left, bool vec) {
+    constexpr int PER = 16 / int(sizeof(T));
+    if (vec && left >= COLS) {
+#pragma unroll
+        for (int j = 0; j < COLS; j += PER) {
+            T t[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) t[i] = from_f32<T>(v[j + i]);
+            *reinterpret_cast<uint4*>(y + j) = *reinterpret_cast<const uint4*>(t);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            if (j < left) y[j] = from_f32<T>(v[j]);
+    }
+}
+template <int COLS>
+__device__ __forceinline__ void store_row_as(const Args& g, int64_t tok, int64_t col, const float* v) {
+    const int64_t left = g.n - col;
+    if (left <= 0) return;
+    const int size = g.out == GPTQ_F32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && (g.ldy * size) % 16 == 0;
+    if (g.out == GPTQ_F32)
+        store_row<float, COLS>(static_cast<float*>(g.y) + tok * g.ldy + col, v, left, vec);
+    else if (g.out == GPTQ_BF16)
+        store_row<__nv_bfloat16, COLS>(static_cast<__nv_bfloat16*>(g.y) + tok * g.ldy + col, v, left, vec);
+    else
+        store_row<__half, COLS>(static_cast<__half*>(g.y) + tok * g.ldy + col, v, left, vec);
+}
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
+    wide_kernel(const __grid_constant__ Maps maps, const Args g) {
+    using C = Wide;
+    constexpr int TILE_N = GATED ? 128 : 256;             // output columns of a tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* ring_all = reinterpret_cast<float*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);
+    uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + C::SUM_WARPS * C::RING * C::SCALES * 32);  // [2][2][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * 2 * 128);   // CTA 0: both CTAs' loads landed
+    uint64_t* empty = full + C::STAGES;     // both CTAs: the pair's MMAs are done with the stage
+    uint64_t* tfull = empty + C::STAGES;    // both CTAs: accumulator complete
+    uint64_t* tempty = tfull + C::SLOTS;    // CTA 0: accumulator read by both CTAs' warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + C::SLOTS);
+
+    const uint32_t rank = cluster_ctarank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // at most 2^16 x 2^15 tiles
+    const uint32_t cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const uint32_t tiles_m = uint32_t((g.m + 255) / 256), tiles_n = uint32_t((g.n + TILE_N - 1) / TILE_N);
+    const uint32_t tiles = tiles_m * tiles_n;
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&maps.w);
+        if (GATED) tma_prefetch_desc(&maps.u);
+        tma_prefetch_desc(&maps.x);
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < C::SLOTS; ++s) {
+            mbar_init(&tfull[s], 1);
+            mbar_init(&tempty[s], 2 * C::SUM_WARPS);
+        }
+        fence_mbar_init();
+    }
+    if (warp == C::SUM_WARPS) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();          // barriers of both CTAs initialized, TMEM allocated
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    if (warp >= C::SUM_WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+        if (warp == C::SUM_WARPS && lane == 0) {
+            // ---------------- loads (both CTAs)
+            const uint32_t full0 = mapa_shared(&full[0], 0);
+            const CUtensorMap* wmap = GATED && rank == 1 ? &maps.u : &maps.w;
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t t = cl; t < tiles && ok; t += ncl) {
+                uint32_t tm, tn;
+                grouped_tile(t, tiles_m, tiles_n, tm, tn);
+                const int xr = int(tm * 256 + rank * 128), wr = int(tn * TILE_N + (GATED ? 0 : rank * 128));
+                for (int b = 0; b < g.nkb; ++b, ++it) {
+                    const uint32_t s = it % C::STAGES, round = it / C::STAGES;
+                    if (!mbar_wait(&empty[s], (round & 1u) ^ 1u, g.st, 411)) { ok = false; break; }
+                    uint8_t* base = smem + size_t(s) * C::STAGE_BYTES;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+                    tma_load_2d_pair(base, &maps.x, b * 128, xr, full0 + s * 8u);
+                    tma_load_2d_pair(base + TILE_BYTES, wmap, b * 128, wr, full0 + s * 8u);
+                }
+            }
+        }
+        if (warp == C::SUM_WARPS + 1 && lane == 0 && rank == 0) {
+            // ---------------- MMAs (CTA 0 for the pair)
+            constexpr uint32_t idesc = idesc_e4m3(256, 256);
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t t = cl; t < tiles && ok; t += ncl) {
+                for (int b = 0; b < g.nkb; ++b, ++it) {
+                    const uint32_t s = it % C::STAGES, d = it % C::SLOTS;
+                    const uint32_t use = it / C::SLOTS;
+                    if (use > 0 && !mbar_wait_cluster(&tempty[d], (use - 1) & 1u, g.st, 412)) { ok = false; break; }
+                    if (!mbar_wait(&full[s], (it / C::STAGES) & 1u, g.st, 413)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t xa = smem_u32(smem + size_t(s) * C::STAGE_BYTES), wa = xa + TILE_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f8_pair(tmem_base + d * 256, sdesc_sw128(xa + kk * 32, 16, 1024),
+                                     sdesc_sw128(wa + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+                    umma_commit_pair_both(&empty[s]);
+                    umma_commit_pair_both(&tfull[d]);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SUM_REGS));
+        // ---------------- sums (both CTAs): lane = token, registers = 128 columns
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
+        float* ring = ring_all + warp * (C::RING * C::SCALES * 32) + lane;
+        // accumulator columns of this thread's first and second 64
+        const uint32_t c0 = GATED ? 64u * half : 128u * half, c1 = GATED ? 128u + 64u * half : c0 + 64u;
+        uint32_t it = 0;
+        uint32_t parity = 0;
+        bool live = true;     // a wait that ran out: go on without waiting, so that all warps meet at the barriers
+        for (uint32_t t = cl; t < tiles; t += ncl, parity ^= 1u) {
+            uint32_t tm, tn;
+            grouped_tile(t, tiles_m, tiles_n, tm, tn);
+            const int64_t tok = int64_t(tm) * 256 + rank * 128 + quad * 32 + lane;
+            const int64_t wrow = GATED ? int64_t(tn) : min(2 * int64_t(tn) + half, (g.n - 1) / 128);   // row of weight scale blocks
+            const float* xs = g.xs + min(tok, g.m - 1);
+            const float* ws = g.ws + wrow * g.nkb;
+            const float* us = GATED ? g.us + wrow * g.nkb : nullptr;
+            auto fetch = [&](int b) {
+                if (b < g.nkb) {
+                    float* at = ring + (b % C::RING) * (C::SCALES * 32);
+                    copy4_async(at, xs + int64_t(b) * g.lds, tok < g.m);
+                    copy4_async(at + 32, ws + b, true);
+                    if (GATED) copy4_async(at + 64, us + b, true);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            float acc[128];
+#pragma unroll
+            for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+            for (int b = 0; b < C::AHEAD; ++b) fetch(b);
+            for (int b = 0; b < g.nkb; ++b, ++it) {
+                const uint32_t d = it % C::SLOTS;
+                fetch(b + C::AHEAD);
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
+                const float* at = ring + (b % C::RING) * (C::SCALES * 32);
+                const float s0 = at[0] * at[32], s1 = GATED ? at[0] * at[64] : s0;
+                if (live) live = mbar_wait(&tfull[d], (it / C::SLOTS) & 1u, g.st, 414);
+                live = __all_sync(0xFFFFFFFFu, live);
+                tc_fence_after();
+                const uint32_t dt = tmem_base + (uint32_t(quad * 32) << 16) + d * 256;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t v[32];
+                    tmem_ld_x32(dt + (j < 2 ? c0 : c1) + 32 * (j & 1), v);
+                    tmem_ld_done(v);
+                    if (j == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + d * 8u);
+                    }
+                    const float s = j < 2 ? s0 : s1;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[32 * j + i] = fmaf(__uint_as_float(v[i]), s, acc[32 * j + i]);
+                }
+            }
+            if (!GATED) {
+                if (tok < g.m) store_row_as<128>(g, tok, int64_t(tn) * 256 + half * 128, acc);
+                continue;
+            }
+            const int64_t col = int64_t(tn) * 128 + half * 64;
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+                acc[c] = gate_act(acc[c], g.act) * acc[64 + c];
+                top = max(top, __float_as_uint(acc[c]) & 0x7FFFFFFFu);
+            }
+            if (g.out != OUT_CODES) {
+                if (tok < g.m) store_row_as<64>(g, tok, col, acc);
+                continue;
+            }
+            // the block's maximum is over this thread's 64 columns and the other half's
+            const int r = quad * 32 + lane;
+            amax[parity * 256 + half * 128 + r] = top;
+            named_barrier_sync(1, 32 * C::SUM_WARPS);
+            top = max(top, amax[parity * 256 + (half ^ 1) * 128 + r]);
+            if (tok >= g.m) continue;
+            float s = block_scale(top);
+            if (half == 0) {
+                g.ys[int64_t(tn) * g.ldys + tok] = s;
+                if (top >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, int(tok));
+            }
+            if (s < SMALL_SCALE) {
+                s *= SMALL_LIFT;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) acc[c] *= SMALL_LIFT;
+            }
+            const float y = __frcp_rn(s);
+            uint8_t* out = static_cast<uint8_t*>(g.y) + tok * g.ldy + col;
+            const int64_t left = g.n - col;
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                const uint4 q = make_uint4(codes4(acc + c, s, y), codes4(acc + c + 4, s, y), codes4(acc + c + 8, s, y),
+                                           codes4(acc + c + 12, s, y));
+                if (left >= c + 16) {
+                    *reinterpret_cast<uint4*>(out + c) = q;
+                } else {
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < left) out[c + i] = uint8_t(w[i / 4] >> (8 * (i & 3)));
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();          // no remote arrival or pair MMA is still pending
+    if (warp == C::SUM_WARPS) tmem_dealloc_pair(tmem_base, 512);
+}
+
 }  // namespace fp8
 
 namespace {
@@ -386,9 +695,51 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
     return GPTQ_OK;
 }
 
+template <bool GATED>
+int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
+    auto kernel = fp8::wide_kernel<GATED>;
+    static std::atomic<bool> ready[kMaxDev];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || sm_count(dev, &sms)) return GPTQ_ERR_CUDA;
+    if (!ready[dev].load()) {
+        using C = fp8::Wide;
+        cudaFuncAttributes attr;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM_BYTES)) !=
+                cudaSuccess ||
+            cudaFuncGetAttributes(&attr, kernel) != cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        // the kernel's warpgroups exchange registers: more than the launch holds would wait for good
+        if (attr.numRegs * C::THREADS < 32 * C::SUM_WARPS * C::SUM_REGS + 128 * C::OTHER_REGS) return GPTQ_ERR_CUDA;
+        ready[dev].store(true);
+    }
+    fp8::Maps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    int rc = make_code_map(encode, &maps.w, p.w, p.n, p.d, p.ldw, 128);
+    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, 128);
+    if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, 128);
+    if (rc) return rc;
+    const fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out,
+                      p.act, st};
+    const int64_t tile_n = GATED ? 128 : 256;
+    const int64_t tiles = (p.m + 255) / 256 * ((p.n + tile_n - 1) / tile_n);
+    const unsigned clusters = unsigned(std::min<int64_t>(tiles, sms / 2));
+    if (launch_pdl(kernel, dim3(2 * clusters), dim3(fp8::Wide::THREADS), fp8::Wide::SMEM_BYTES, stream, maps, g) !=
+        cudaSuccess)
+        return GPTQ_ERR_CUDA;
+    count_launch();
+    return GPTQ_OK;
+}
+
+// Tokens from which a product runs on SM pairs.  A build-time tuning knob.
+#ifndef GPTQ_FP8_WIDE_MIN_M
+#define GPTQ_FP8_WIDE_MIN_M 129
+#endif
+
 }  // namespace
 
 int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
+    if (p.m >= GPTQ_FP8_WIDE_MIN_M)
+        return p.u ? launch_wide<true>(p, stream, st, encode) : launch_wide<false>(p, stream, st, encode);
     if (p.u) {
         if (p.m <= 16) return launch_narrow<16, true>(p, stream, st, encode);
         if (p.m <= 32) return launch_narrow<32, true>(p, stream, st, encode);
