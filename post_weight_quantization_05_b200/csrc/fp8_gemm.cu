@@ -37,7 +37,7 @@ struct Args {
     const float *xs, *ws, *us;
     void* y;
     float* ys;
-    int nkb, out, act;
+    int nkb, out;
     DevStatus* st;
 };
 
@@ -81,10 +81,25 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
-// act(g): 0 silu, g / (1 + e^-g); 1 gelu in its exact form, g Phi(g), with Phi
-// from erfc so that large negative gates keep their relative accuracy.
-__device__ __forceinline__ float gate_act(float g, int act) {
-    if (act == 0) return g / (1.0f + expf(-g));
+// e^x = 2^t e^(r ln 2) with t = RN(x log2 e) and r what that rounding and the
+// constant's lost, a number below 2^-16 for every x that matters: 1 + r ln 2
+// is exact enough, and ex2's own error (2^-22) is what remains.
+__device__ __forceinline__ float exp_of(float x) {
+    constexpr float L = 1.44269504f, L_LOW = 1.92596299e-8f;   // log2(e) = L + L_LOW
+    const float t = x * L;
+    const float r = fmaf(x, L_LOW, fmaf(x, L, -t));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return fmaf(e, r * 0.693147181f, e);
+}
+
+// act(g): SILU, g / (1 + e^-g); GELU in its exact form, g Phi(g), with Phi
+// from erfc so that large negative gates keep their relative accuracy.  e^-g
+// that overflows divides to zero.
+constexpr int SILU = 0, GELU = 1;
+template <int ACT>
+__device__ __forceinline__ float gate_act(float g) {
+    if (ACT == SILU) return __fdividef(g, 1.0f + exp_of(fminf(-g, 88.0f)));
     return 0.5f * g * erfcf(g * -0.70710678118654752f);
 }
 
@@ -120,7 +135,7 @@ struct Narrow {
     static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0, "TMEM columns");
 };
 
-template <int NT, bool GATED>
+template <int NT, bool GATED, int ACT>
 __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     narrow_kernel(const __grid_constant__ Maps maps, const Args g) {
     using C = Narrow<NT, GATED>;
@@ -278,7 +293,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                 v += ld_cluster_f32(mapa_shared(part + c * 128 + r, q));
                 if (GATED) u += ld_cluster_f32(mapa_shared(part + (NT + c) * 128 + r, q));
             }
-            if (GATED) v = gate_act(v, g.act) * u;
+            if (GATED) v = gate_act<ACT>(v) * u;
             if (GATED && g.out == OUT_CODES) {
                 held[c * 128 + r] = v;
                 const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
@@ -326,6 +341,8 @@ struct Wide {
     static constexpr int STAGES = 6;
     static constexpr int SLOTS = 2;
     static constexpr int SUM_WARPS = 8;
+    static constexpr int PARTS = SUM_WARPS / 4;           // threads that share a token's columns
+    static constexpr int CPT = 256 / PARTS;               // columns of a thread
     static constexpr int THREADS = 32 * (SUM_WARPS + 4);  // and a warp each for loads and MMAs, two idle
     // Registers per thread after the split between the sums' two warpgroups and
     // the third; the launch checks that they fit what it was given.
@@ -334,7 +351,7 @@ struct Wide {
     static constexpr int RING = 8;                        // blocks of scales per warp
     static constexpr int SCALES = 3;                      // token, weight, second weight
     static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * RING * SCALES * 32 * 4 +
-                                         2 * 2 * 128 * 4 + (2 * STAGES + 2 * SLOTS) * 8 + 16;
+                                         2 * PARTS * 128 * 4 + (2 * STAGES + 2 * SLOTS) * 8 + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -347,17 +364,16 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, ui
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
+// a[0..1] += v[0..1] * s (one instruction).
+__device__ __forceinline__ void fma2(float* a, const uint32_t* v, float s) {
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%0, %1};\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "mov.b64 z, {%4, %4};\n\t"
+        "fma.rn.f32x2 x, y, z, x;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a[0]), "+f"(a[1])
+        : "r"(v[0]), "r"(v[1]), "f"(s));
 }
 // Arrive on an mbarrier of either CTA without publishing memory: for an
 // accumulator that has been read (its loads have returned) nothing else needs
@@ -416,7 +432,7 @@ __device__ __forceinline__ void store_row_as(const Args& g, int64_t tok, int64_t
         store_row<__half, COLS>(static_cast<__half*>(g.y) + tok * g.ldy + col, v, left, vec);
 }
 
-template <bool GATED>
+template <bool GATED, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     wide_kernel(const __grid_constant__ Maps maps, const Args g) {
     using C = Wide;
@@ -424,8 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* ring_all = reinterpret_cast<float*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);
-    uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + C::SUM_WARPS * C::RING * C::SCALES * 32);  // [2][2][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * 2 * 128);   // CTA 0: both CTAs' loads landed
+    uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + C::SUM_WARPS * C::RING * C::SCALES * 32);  // [2][PARTS][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * C::PARTS * 128);   // CTA 0: both CTAs' loads landed
     uint64_t* empty = full + C::STAGES;     // both CTAs: the pair's MMAs are done with the stage
     uint64_t* tfull = empty + C::STAGES;    // both CTAs: accumulator complete
     uint64_t* tempty = tfull + C::SLOTS;    // CTA 0: accumulator read by both CTAs' warps
@@ -510,11 +526,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SUM_REGS));
         // ---------------- sums (both CTAs): lane = token, registers = 128 columns
-        const int quad = warp & 3, half = warp >> 2;
+        const int quad = warp & 3, part = warp >> 2;
+        constexpr int CPT = C::CPT, PARTS = C::PARTS;
         const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
         float* ring = ring_all + warp * (C::RING * C::SCALES * 32) + lane;
-        // accumulator columns of this thread's first and second 64
-        const uint32_t c0 = GATED ? 64u * half : 128u * half, c1 = GATED ? 128u + 64u * half : c0 + 64u;
+        // accumulator columns of the two halves of this thread's sums (gated: gate and up)
+        const uint32_t c0 = GATED ? (CPT / 2) * part : CPT * part, c1 = GATED ? 128 + c0 : c0 + CPT / 2;
         uint32_t it = 0;
         uint32_t parity = 0;
         bool live = true;     // a wait that ran out: go on without waiting, so that all warps meet at the barriers
@@ -522,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
             uint32_t tm, tn;
             grouped_tile(t, tiles_m, tiles_n, tm, tn);
             const int64_t tok = int64_t(tm) * 256 + rank * 128 + quad * 32 + lane;
-            const int64_t wrow = GATED ? int64_t(tn) : min(2 * int64_t(tn) + half, (g.n - 1) / 128);   // row of weight scale blocks
+            const int64_t wrow = GATED ? int64_t(tn) : min(2 * int64_t(tn) + part * 2 / PARTS, (g.n - 1) / 128);   // row of weight scale blocks
             const float* xs = g.xs + min(tok, g.m - 1);
             const float* ws = g.ws + wrow * g.nkb;
             const float* us = GATED ? g.us + wrow * g.nkb : nullptr;
@@ -535,9 +552,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            float acc[128];
+            float acc[CPT];
 #pragma unroll
-            for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+            for (int c = 0; c < CPT; ++c) acc[c] = 0.0f;
             for (int b = 0; b < C::AHEAD; ++b) fetch(b);
             for (int b = 0; b < g.nkb; ++b, ++it) {
                 const uint32_t d = it % C::SLOTS;
@@ -549,57 +566,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 live = __all_sync(0xFFFFFFFFu, live);
                 tc_fence_after();
                 const uint32_t dt = tmem_base + (uint32_t(quad * 32) << 16) + d * 256;
+                // 16 columns at a time, the next ones on their way while these are added
+                constexpr int STEPS = CPT / 16;
+                auto column = [&](int j) { return dt + (j < STEPS / 2 ? c0 + 16 * j : c1 + 16 * (j - STEPS / 2)); };
+                uint32_t v[2][16];
+                tmem_ld_x16(column(0), v[0]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t v[32];
-                    tmem_ld_x32(dt + (j < 2 ? c0 : c1) + 32 * (j & 1), v);
-                    tmem_ld_done(v);
-                    if (j == 3) {
+                for (int j = 0; j < STEPS; ++j) {
+                    tmem_ld_done(v[j & 1]);
+                    if (j + 1 < STEPS) {
+                        tmem_ld_x16(column(j + 1), v[(j + 1) & 1]);
+                    } else {                  // this warp has read its part of the accumulator
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + d * 8u);
                     }
-                    const float s = j < 2 ? s0 : s1;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[32 * j + i] = fmaf(__uint_as_float(v[i]), s, acc[32 * j + i]);
+                    for (int i = 0; i < 16; i += 2)
+                        fma2(acc + 16 * j + i, v[j & 1] + i, j < STEPS / 2 ? s0 : s1);
                 }
             }
             if (!GATED) {
-                if (tok < g.m) store_row_as<128>(g, tok, int64_t(tn) * 256 + half * 128, acc);
+                if (tok < g.m) store_row_as<CPT>(g, tok, int64_t(tn) * 256 + part * CPT, acc);
                 continue;
             }
-            const int64_t col = int64_t(tn) * 128 + half * 64;
+            constexpr int OC = CPT / 2;
+            const int64_t col = int64_t(tn) * 128 + part * OC;
             uint32_t top = 0;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                acc[c] = gate_act(acc[c], g.act) * acc[64 + c];
+            for (int c = 0; c < OC; ++c) {
+                acc[c] = gate_act<ACT>(acc[c]) * acc[OC + c];
                 top = max(top, __float_as_uint(acc[c]) & 0x7FFFFFFFu);
             }
             if (g.out != OUT_CODES) {
-                if (tok < g.m) store_row_as<64>(g, tok, col, acc);
+                if (tok < g.m) store_row_as<OC>(g, tok, col, acc);
                 continue;
             }
-            // the block's maximum is over this thread's 64 columns and the other half's
+            // the block's maximum is over this thread's columns and the other parts'
             const int r = quad * 32 + lane;
-            amax[parity * 256 + half * 128 + r] = top;
+            amax[(parity * PARTS + part) * 128 + r] = top;
             named_barrier_sync(1, 32 * C::SUM_WARPS);
-            top = max(top, amax[parity * 256 + (half ^ 1) * 128 + r]);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) top = max(top, amax[(parity * PARTS + q) * 128 + r]);
             if (tok >= g.m) continue;
             float s = block_scale(top);
-            if (half == 0) {
+            if (part == 0) {
                 g.ys[int64_t(tn) * g.ldys + tok] = s;
                 if (top >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, int(tok));
             }
             if (s < SMALL_SCALE) {
                 s *= SMALL_LIFT;
 #pragma unroll
-                for (int c = 0; c < 64; ++c) acc[c] *= SMALL_LIFT;
+                for (int c = 0; c < OC; ++c) acc[c] *= SMALL_LIFT;
             }
             const float y = __frcp_rn(s);
             uint8_t* out = static_cast<uint8_t*>(g.y) + tok * g.ldy + col;
             const int64_t left = g.n - col;
 #pragma unroll
-            for (int c = 0; c < 64; c += 16) {
+            for (int c = 0; c < OC; c += 16) {
                 const uint4 q = make_uint4(codes4(acc + c, s, y), codes4(acc + c + 4, s, y), codes4(acc + c + 8, s, y),
                                            codes4(acc + c + 12, s, y));
                 if (left >= c + 16) {
@@ -650,10 +674,10 @@ int sm_count(int dev, int* out) {
     return GPTQ_OK;
 }
 
-template <int NT, bool GATED>
+template <int NT, bool GATED, int ACT = 0>
 int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
     using C = fp8::Narrow<NT, GATED>;
-    auto kernel = fp8::narrow_kernel<NT, GATED>;
+    auto kernel = fp8::narrow_kernel<NT, GATED, ACT>;
     static std::atomic<int> per_sm[kMaxDev];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || sm_count(dev, &sms)) return GPTQ_ERR_CUDA;
@@ -671,7 +695,7 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
     if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, 128);
     if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, NT);
     if (rc) return rc;
-    fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, p.act, st};
+    fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, st};
     // As many CTAs per tile as fill the GPU once, up to a portable cluster.
     const int64_t rows = (p.n + 127) / 128, toks = (p.m + NT - 1) / NT;
     const int64_t split = std::max<int64_t>(
@@ -695,9 +719,9 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
     return GPTQ_OK;
 }
 
-template <bool GATED>
+template <bool GATED, int ACT = 0>
 int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
-    auto kernel = fp8::wide_kernel<GATED>;
+    auto kernel = fp8::wide_kernel<GATED, ACT>;
     static std::atomic<bool> ready[kMaxDev];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || sm_count(dev, &sms)) return GPTQ_ERR_CUDA;
@@ -719,7 +743,7 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
     if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, 128);
     if (rc) return rc;
     const fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out,
-                      p.act, st};
+                      st};
     const int64_t tile_n = GATED ? 128 : 256;
     const int64_t tiles = (p.m + 255) / 256 * ((p.n + tile_n - 1) / tile_n);
     const unsigned clusters = unsigned(std::min<int64_t>(tiles, sms / 2));
@@ -737,14 +761,19 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
 
 }  // namespace
 
+template <int ACT>
+static int launch_gated(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
+    if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<true, ACT>(p, stream, st, encode);
+    if (p.m <= 16) return launch_narrow<16, true, ACT>(p, stream, st, encode);
+    if (p.m <= 32) return launch_narrow<32, true, ACT>(p, stream, st, encode);
+    return launch_narrow<64, true, ACT>(p, stream, st, encode);
+}
+
 int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
-    if (p.m >= GPTQ_FP8_WIDE_MIN_M)
-        return p.u ? launch_wide<true>(p, stream, st, encode) : launch_wide<false>(p, stream, st, encode);
-    if (p.u) {
-        if (p.m <= 16) return launch_narrow<16, true>(p, stream, st, encode);
-        if (p.m <= 32) return launch_narrow<32, true>(p, stream, st, encode);
-        return launch_narrow<64, true>(p, stream, st, encode);
-    }
+    if (p.u)
+        return p.act == fp8::SILU ? launch_gated<fp8::SILU>(p, stream, st, encode)
+                                  : launch_gated<fp8::GELU>(p, stream, st, encode);
+    if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<false>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, false>(p, stream, st, encode);
     if (p.m <= 32) return launch_narrow<32, false>(p, stream, st, encode);
     if (p.m <= 64) return launch_narrow<64, false>(p, stream, st, encode);
