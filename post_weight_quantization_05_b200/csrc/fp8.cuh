@@ -48,10 +48,23 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Four codes of four values of a block with scale s, y = RN(1 / s).
+// Four codes of four values of a block with scale s, y = RN(1 / s).  x y is
+// within two units in the last place of x / s, so unless one of the four lies
+// within four of a number of at most five leading bits (the middles among
+// them), rounding x y gives the codes.
 __device__ __forceinline__ uint32_t codes4(const float* v, float s, float y) {
-    return e4m3x2(quotient(v[0], s, y), quotient(v[1], s, y)) |
-           (e4m3x2(quotient(v[2], s, y), quotient(v[3], s, y)) << 16);
+    float q[4];
+    uint32_t near = ~0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q[i] = __fmul_rn(v[i], y);
+        near = min(near, (__float_as_uint(q[i]) + 4u) & 0x7FFF8u);
+    }
+    if (near == 0u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = quotient(v[i], s, y);
+    }
+    return e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
 }
 
 // Blocks whose scale is below this take their values and scale times

@@ -94,12 +94,16 @@ __device__ __forceinline__ float exp_of(float x) {
 }
 
 // act(g): SILU, g / (1 + e^-g); GELU in its exact form, g Phi(g), with Phi
-// from erfc so that large negative gates keep their relative accuracy.  e^-g
-// that overflows divides to zero.
+// from erfc so that large negative gates keep their relative accuracy.  The
+// reciprocal of e^88 is below the normal numbers and counts as 0.
 constexpr int SILU = 0, GELU = 1;
 template <int ACT>
 __device__ __forceinline__ float gate_act(float g) {
-    if (ACT == SILU) return __fdividef(g, 1.0f + exp_of(fminf(-g, 88.0f)));
+    if (ACT == SILU) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_of(fminf(-g, 88.0f))));
+        return g * r;
+    }
     return 0.5f * g * erfcf(g * -0.70710678118654752f);
 }
 
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
 // clock that shared memory gives at the tensor cores' e4m3 rate.
 struct Wide {
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = 4;                      // three to six measured the same
     static constexpr int SLOTS = 2;
     static constexpr int SUM_WARPS = 8;
     static constexpr int PARTS = SUM_WARPS / 4;           // threads that share a token's columns
@@ -350,8 +354,10 @@ struct Wide {
     static constexpr int AHEAD = 4;                       // blocks of scales in flight per thread
     static constexpr int RING = 8;                        // blocks of scales per warp
     static constexpr int SCALES = 3;                      // token, weight, second weight
-    static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * RING * SCALES * 32 * 4 +
-                                         2 * PARTS * 128 * 4 + (2 * STAGES + 2 * SLOTS) * 8 + 16;
+    static constexpr int OUT_BYTES = 32 * 256;            // per warp: 256 bytes of 32 output rows on their way out
+    static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * OUT_BYTES +
+                                         SUM_WARPS * RING * SCALES * 32 * 4 + 2 * PARTS * 128 * 4 +
+                                         (2 * STAGES + SLOTS) * 8 + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -400,36 +406,71 @@ __device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t tiles_m, uint3
     tn = in / rows;
 }
 
-// COLS consecutive values of one output row; `vec`: 16-byte stores are aligned.
-template <typename T, int COLS>
-__device__ __forceinline__ void store_row(T* y, const float* v, int64_t left, bool vec) {
-    constexpr int PER = 16 / int(sizeof(T));
-    if (vec && left >= COLS) {
+// A warp's 32 output rows of RB bytes (a power of two, 64 .. 256), staged in
+// shared memory: lane r writes row r, then the lanes write whole pieces of rows
+// to global memory (straight from the registers each 16-byte store of a warp
+// would touch 32 lines).  at(): where 16-byte chunk c of row r is kept, so that
+// neither side's eight-lane phases meet in a bank.
+template <int RB>
+struct Stage {
+    static constexpr int CHUNKS = RB / 16;
+    static __device__ __forceinline__ int at(int r, int c) {
+        return r * RB + ((c ^ (CHUNKS == 4 ? (r >> 1) & 3 : r & 7)) << 4);
+    }
+    // rows x cols elements of T go to y (row pitch ld elements); vec: y and ld allow 16-byte stores.
+    template <typename T>
+    static __device__ __forceinline__ void flush(const uint8_t* buf, T* y, int64_t ld, int rows, int cols, bool vec,
+                                                 int lane) {
+        __syncwarp();
+        if (vec && cols == RB / int(sizeof(T))) {
 #pragma unroll
-        for (int j = 0; j < COLS; j += PER) {
-            T t[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) t[i] = from_f32<T>(v[j + i]);
-            *reinterpret_cast<uint4*>(y + j) = *reinterpret_cast<const uint4*>(t);
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int r = i * (32 / CHUNKS) + lane / CHUNKS, c = lane % CHUNKS;
+                if (r < rows)
+                    *reinterpret_cast<uint4*>(y + r * ld + c * (16 / int(sizeof(T)))) =
+                        *reinterpret_cast<const uint4*>(buf + at(r, c));
+            }
+        } else {
+            for (int r = 0; r < rows; ++r)
+                for (int c = lane; c < cols; c += 32) {
+                    const int byte = c * int(sizeof(T));
+                    y[r * ld + c] = *reinterpret_cast<const T*>(buf + at(r, byte >> 4) + (byte & 15));
+                }
         }
-    } else {
+        __syncwarp();
+    }
+};
+
+// COLS values per lane (one output row each) as T.
+template <typename T, int COLS>
+__device__ __forceinline__ void store_rows(uint8_t* buf, T* y, int64_t ld, int rows, int64_t left, bool vec, int lane,
+                                           const float* v) {
+    constexpr int PER = 16 / int(sizeof(T)), RB = COLS * int(sizeof(T)) < 256 ? COLS * int(sizeof(T)) : 256;
+    constexpr int PASS = RB / int(sizeof(T));
 #pragma unroll
-        for (int j = 0; j < COLS; ++j)
-            if (j < left) y[j] = from_f32<T>(v[j]);
+    for (int p = 0; p < COLS; p += PASS) {
+#pragma unroll
+        for (int j = 0; j < PASS; j += PER) {
+            __align__(16) T t[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) t[i] = from_f32<T>(v[p + j + i]);
+            *reinterpret_cast<uint4*>(buf + Stage<RB>::at(lane, j / PER)) = *reinterpret_cast<const uint4*>(t);
+        }
+        Stage<RB>::flush(buf, y + p, ld, rows, int(max(int64_t(0), min(left - p, int64_t(PASS)))), vec, lane);
     }
 }
 template <int COLS>
-__device__ __forceinline__ void store_row_as(const Args& g, int64_t tok, int64_t col, const float* v) {
-    const int64_t left = g.n - col;
-    if (left <= 0) return;
-    const int size = g.out == GPTQ_F32 ? 4 : 2;
-    const bool vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && (g.ldy * size) % 16 == 0;
+__device__ __forceinline__ void store_rows_as(const Args& g, uint8_t* buf, int64_t tok0, int64_t col, int lane,
+                                              const float* v) {
+    const int rows = int(max(int64_t(0), min(g.m - tok0, int64_t(32))));
+    const int64_t left = g.n - col, at = tok0 * g.ldy + col;
+    const bool vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && (g.ldy * (g.out == GPTQ_F32 ? 4 : 2)) % 16 == 0;
     if (g.out == GPTQ_F32)
-        store_row<float, COLS>(static_cast<float*>(g.y) + tok * g.ldy + col, v, left, vec);
+        store_rows<float, COLS>(buf, static_cast<float*>(g.y) + at, g.ldy, rows, left, vec, lane, v);
     else if (g.out == GPTQ_BF16)
-        store_row<__nv_bfloat16, COLS>(static_cast<__nv_bfloat16*>(g.y) + tok * g.ldy + col, v, left, vec);
+        store_rows<__nv_bfloat16, COLS>(buf, static_cast<__nv_bfloat16*>(g.y) + at, g.ldy, rows, left, vec, lane, v);
     else
-        store_row<__half, COLS>(static_cast<__half*>(g.y) + tok * g.ldy + col, v, left, vec);
+        store_rows<__half, COLS>(buf, static_cast<__half*>(g.y) + at, g.ldy, rows, left, vec, lane, v);
 }
 
 template <bool GATED, int ACT>
@@ -439,12 +480,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     constexpr int TILE_N = GATED ? 128 : 256;             // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* ring_all = reinterpret_cast<float*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);
+    uint8_t* out_all = smem + size_t(C::STAGES) * C::STAGE_BYTES;
+    float* ring_all = reinterpret_cast<float*>(out_all + C::SUM_WARPS * C::OUT_BYTES);
     uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + C::SUM_WARPS * C::RING * C::SCALES * 32);  // [2][PARTS][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * C::PARTS * 128);   // CTA 0: both CTAs' loads landed
-    uint64_t* empty = full + C::STAGES;     // both CTAs: the pair's MMAs are done with the stage
-    uint64_t* tfull = empty + C::STAGES;    // both CTAs: accumulator complete
-    uint64_t* tempty = tfull + C::SLOTS;    // CTA 0: accumulator read by both CTAs' warps
+    uint64_t* done = full + C::STAGES;      // both CTAs: the pair's MMAs of the stage's block are complete
+    uint64_t* tempty = done + C::STAGES;    // CTA 0: accumulator read by both CTAs' warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + C::SLOTS);
 
     const uint32_t rank = cluster_ctarank();
@@ -460,12 +501,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
         tma_prefetch_desc(&maps.x);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&done[s], 1);
         }
-        for (int s = 0; s < C::SLOTS; ++s) {
-            mbar_init(&tfull[s], 1);
-            mbar_init(&tempty[s], 2 * C::SUM_WARPS);
-        }
+        for (int s = 0; s < C::SLOTS; ++s) mbar_init(&tempty[s], 2 * C::SUM_WARPS);
         fence_mbar_init();
     }
     if (warp == C::SUM_WARPS) {
@@ -493,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 const int xr = int(tm * 256 + rank * 128), wr = int(tn * TILE_N + (GATED ? 0 : rank * 128));
                 for (int b = 0; b < g.nkb; ++b, ++it) {
                     const uint32_t s = it % C::STAGES, round = it / C::STAGES;
-                    if (!mbar_wait(&empty[s], (round & 1u) ^ 1u, g.st, 411)) { ok = false; break; }
+                    if (!mbar_wait(&done[s], (round & 1u) ^ 1u, g.st, 411)) { ok = false; break; }
                     uint8_t* base = smem + size_t(s) * C::STAGE_BYTES;
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
                     tma_load_2d_pair(base, &maps.x, b * 128, xr, full0 + s * 8u);
@@ -518,8 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                     for (int kk = 0; kk < 4; ++kk)
                         umma_f8_pair(tmem_base + d * 256, sdesc_sw128(xa + kk * 32, 16, 1024),
                                      sdesc_sw128(wa + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-                    umma_commit_pair_both(&empty[s]);
-                    umma_commit_pair_both(&tfull[d]);
+                    umma_commit_pair_both(&done[s]);   // frees the stage and completes the accumulator
                 }
             }
         }
@@ -529,6 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
         const int quad = warp & 3, part = warp >> 2;
         constexpr int CPT = C::CPT, PARTS = C::PARTS;
         const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
+        uint8_t* out_buf = out_all + warp * C::OUT_BYTES;
         float* ring = ring_all + warp * (C::RING * C::SCALES * 32) + lane;
         // accumulator columns of the two halves of this thread's sums (gated: gate and up)
         const uint32_t c0 = GATED ? (CPT / 2) * part : CPT * part, c1 = GATED ? 128 + c0 : c0 + CPT / 2;
@@ -562,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
                 const float* at = ring + (b % C::RING) * (C::SCALES * 32);
                 const float s0 = at[0] * at[32], s1 = GATED ? at[0] * at[64] : s0;
-                if (live) live = mbar_wait(&tfull[d], (it / C::SLOTS) & 1u, g.st, 414);
+                if (live) live = mbar_wait(&done[it % C::STAGES], (it / C::STAGES) & 1u, g.st, 414);
                 live = __all_sync(0xFFFFFFFFu, live);
                 tc_fence_after();
                 const uint32_t dt = tmem_base + (uint32_t(quad * 32) << 16) + d * 256;
@@ -587,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 }
             }
             if (!GATED) {
-                if (tok < g.m) store_row_as<CPT>(g, tok, int64_t(tn) * 256 + part * CPT, acc);
+                store_rows_as<CPT>(g, out_buf, tok - lane, int64_t(tn) * 256 + part * CPT, lane, acc);
                 continue;
             }
             constexpr int OC = CPT / 2;
@@ -599,7 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 top = max(top, __float_as_uint(acc[c]) & 0x7FFFFFFFu);
             }
             if (g.out != OUT_CODES) {
-                if (tok < g.m) store_row_as<OC>(g, tok, col, acc);
+                store_rows_as<OC>(g, out_buf, tok - lane, col, lane, acc);
                 continue;
             }
             // the block's maximum is over this thread's columns and the other parts'
@@ -608,9 +646,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
             named_barrier_sync(1, 32 * C::SUM_WARPS);
 #pragma unroll
             for (int q = 0; q < PARTS; ++q) top = max(top, amax[(parity * PARTS + q) * 128 + r]);
-            if (tok >= g.m) continue;
             float s = block_scale(top);
-            if (part == 0) {
+            if (part == 0 && tok < g.m) {
                 g.ys[int64_t(tn) * g.ldys + tok] = s;
                 if (top >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, int(tok));
             }
@@ -620,21 +657,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 for (int c = 0; c < OC; ++c) acc[c] *= SMALL_LIFT;
             }
             const float y = __frcp_rn(s);
-            uint8_t* out = static_cast<uint8_t*>(g.y) + tok * g.ldy + col;
-            const int64_t left = g.n - col;
 #pragma unroll
-            for (int c = 0; c < OC; c += 16) {
-                const uint4 q = make_uint4(codes4(acc + c, s, y), codes4(acc + c + 4, s, y), codes4(acc + c + 8, s, y),
-                                           codes4(acc + c + 12, s, y));
-                if (left >= c + 16) {
-                    *reinterpret_cast<uint4*>(out + c) = q;
-                } else {
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c + i < left) out[c + i] = uint8_t(w[i / 4] >> (8 * (i & 3)));
-                }
-            }
+            for (int c = 0; c < OC; c += 16)
+                *reinterpret_cast<uint4*>(out_buf + Stage<OC>::at(lane, c / 16)) =
+                    make_uint4(codes4(acc + c, s, y), codes4(acc + c + 4, s, y), codes4(acc + c + 8, s, y),
+                               codes4(acc + c + 12, s, y));
+            Stage<OC>::flush(out_buf, static_cast<uint8_t*>(g.y) + (tok - lane) * g.ldy + col, g.ldy,
+                             int(max(int64_t(0), min(g.m - (tok - lane), int64_t(32)))),
+                             int(max(int64_t(0), min(g.n - col, int64_t(OC)))), true, lane);
         }
     }
     __syncwarp();
