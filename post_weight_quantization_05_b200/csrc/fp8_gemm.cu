@@ -100,9 +100,7 @@ constexpr int SILU = 0, GELU = 1;
 template <int ACT>
 __device__ __forceinline__ float gate_act(float g) {
     if (ACT == SILU) {
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_of(fminf(-g, 88.0f))));
-        return g * r;
+        return g * rcp_approx(1.0f + exp_of(fminf(-g, 88.0f)));
     }
     return 0.5f * g * erfcf(g * -0.70710678118654752f);
 }
@@ -321,7 +319,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                 }
                 if (row < g.n)
                     static_cast<uint8_t*>(g.y)[(tok0 + c) * g.ldy + row] =
-                        uint8_t(e4m3x2(quotient(v, s, __frcp_rn(s)), 0.0f));
+                        uint8_t(code1(v, s, rcp_approx(s)));
             }
         }
     }
@@ -656,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < OC; ++c) acc[c] *= SMALL_LIFT;
             }
-            const float y = __frcp_rn(s);
+            const float y = rcp_approx(s);
 #pragma unroll
             for (int c = 0; c < OC; c += 16)
                 *reinterpret_cast<uint4*>(out_buf + Stage<OC>::at(lane, c / 16)) =

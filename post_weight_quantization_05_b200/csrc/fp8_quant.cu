@@ -19,8 +19,56 @@ constexpr int CHUNK = 256 * UNROLL;   // values of a row one warp takes
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// What a block's codes are made with.
+struct Scale {
+    float s, y;     // the scale and its reciprocal, both lifted for a small one
+    bool small;
+    __device__ __forceinline__ explicit Scale(float scale) {
+        small = scale < SMALL_SCALE;
+        s = small ? scale * SMALL_LIFT : scale;
+        y = rcp_approx(s);
+    }
+};
+__device__ __forceinline__ uint2 codes8(float* v, const Scale& c) {
+    if (c.small) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= SMALL_LIFT;
+    }
+    return make_uint2(codes4(v, c.s, c.y), codes4(v + 4, c.s, c.y));
+}
+__device__ __forceinline__ void store8(uint8_t* out, uint2 c, int64_t n) {
+    if (n >= 8) {
+        *reinterpret_cast<uint2*>(out) = c;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) out[i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+    }
+}
+
+// The maxima over each half warp of UNROLL values of top8(), two 16-bit ones to a word.
+template <typename T>
+__device__ __forceinline__ void half_warp_tops(uint32_t (&a)[UNROLL]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) a[u] = max(a[u], __shfl_xor_sync(0xFFFFFFFFu, a[u], o));
+    } else {
+#pragma unroll
+        for (int u = 0; u < UNROLL; u += 2) {
+            uint32_t p = __vmaxu2(__byte_perm(a[u], a[u + 1], 0x5410), __byte_perm(a[u], a[u + 1], 0x7632));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) p = __vmaxu2(p, __shfl_xor_sync(0xFFFFFFFFu, p, o));
+            a[u] = p & 0xFFFFu;
+            a[u + 1] = p >> 16;
+        }
+    }
+}
+
 // Rows, aligned: 16 lanes hold one block, 8 values a lane, so a block's
-// maximum is four shuffles and its codes leave as 8-byte stores.
+// maximum is four shuffles and its codes leave as 8-byte stores.  A warp has
+// eight blocks in flight; one lane each computes their scales.
 template <typename T>
 __global__ void __launch_bounds__(32 * WARPS)
     quant_rows_kernel(const T* __restrict__ x, int64_t m, int64_t d, int64_t ldx, uint8_t* __restrict__ codes,
@@ -32,46 +80,35 @@ __global__ void __launch_bounds__(32 * WARPS)
     const int64_t k0 = int64_t(blockIdx.x % chunks) * CHUNK + lane * 8;
     if (row >= m) return;
     const T* xr = x + row * ldx;
-    float v[UNROLL][8];
+    Raw8<T> v[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         const int64_t k = k0 + u * 256;
-        if (k + 8 <= d) {
-            load8(xr + k, v[u]);
-        } else {
+        v[u] = k + 8 <= d ? load_raw8(xr + k) : load_some8(xr + k, d - k);
+    }
+    uint32_t a[UNROLL];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = k + i < d ? to_f32(xr[k + i]) : 0.0f;
-        }
+    for (int u = 0; u < UNROLL; ++u) a[u] = top8(v[u]);
+    half_warp_tops<T>(a);
+    const int mine = lane & (UNROLL - 1);
+    uint32_t own = a[0];
+#pragma unroll
+    for (int u = 1; u < UNROLL; ++u) own = mine == u ? a[u] : own;
+    own = top_bits<T>(own);
+    const float scale = block_scale(own);
+    const int64_t block = (k0 - (lane & 15) * 8 + mine * 256) / BLOCK;
+    if ((lane & 15) < UNROLL && block * BLOCK < d) {
+        scales[block * lds + row] = scale;
+        if (own >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(row));
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         const int64_t k = k0 + u * 256;
-        uint32_t a = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[u][i]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-        if (k - (lane & 15) * 8 >= d) continue;             // the block lies behind the row's end
-        float s = block_scale(a);
-        if ((lane & 15) == 0) {
-            scales[(k / BLOCK) * lds + row] = s;
-            if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(min(row, int64_t(0x7FFFFFFF))));
-        }
-        if (s < SMALL_SCALE) {
-            s *= SMALL_LIFT;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] *= SMALL_LIFT;
-        }
-        const float y = __frcp_rn(s);
-        const uint2 c = make_uint2(codes4(v[u], s, y), codes4(v[u] + 4, s, y));
-        uint8_t* out = codes + row * ldc + k;
-        if (k + 8 <= d) {
-            *reinterpret_cast<uint2*>(out) = c;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k + i < d) out[i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
-        }
+        const Scale c(__shfl_sync(0xFFFFFFFFu, scale, (lane & 16) + u));
+        if (k >= d) continue;
+        float f[8];
+        widen8(v[u], f);
+        store8(codes + row * ldc + k, codes8(f, c), d - k);
     }
 }
 
@@ -103,17 +140,17 @@ __global__ void __launch_bounds__(32 * WARPS)
         if (kb >= d) break;
         uint32_t a = max(max(abs_bits(v[b][0]), abs_bits(v[b][1])), max(abs_bits(v[b][2]), abs_bits(v[b][3])));
         a = __reduce_max_sync(0xFFFFFFFFu, a);
-        float s = block_scale(a);
+        const float scale = block_scale(a);
         if (lane == 0) {
-            scales[(kb / BLOCK) * lds + row] = s;
-            if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(min(row, int64_t(0x7FFFFFFF))));
+            scales[(kb / BLOCK) * lds + row] = scale;
+            if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(row));
         }
-        if (s < SMALL_SCALE) {
-            s *= SMALL_LIFT;
+        const Scale sc(scale);
+        if (sc.small) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[b][i] *= SMALL_LIFT;
         }
-        const uint32_t c = codes4(v[b], s, __frcp_rn(s));
+        const uint32_t c = codes4(v[b], sc.s, sc.y);
         uint8_t* out = codes + row * ldc + kb + lane;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -121,78 +158,98 @@ __global__ void __launch_bounds__(32 * WARPS)
     }
 }
 
-// A 128 x 128 block of a weight per thread block, 64 values a thread in
-// registers.  ALIGNED: thread t takes 8 consecutive columns (t % 16) of every
-// sixteenth row; otherwise the columns lane, lane + 32, ... of every eighth.
-template <typename T, bool ALIGNED>
+// A 128 x 128 block of a weight per thread block, aligned: thread t holds 8
+// consecutive columns (t % 16) of every sixteenth row.
+template <typename T>
 __global__ void __launch_bounds__(256)
     quant_weight_kernel(const T* __restrict__ w, int64_t n, int64_t d, int64_t ldw, uint8_t* __restrict__ codes,
                         int64_t ldc, float* __restrict__ scales, int nb, DevStatus* st) {
     __shared__ uint32_t part[8];
     pdl_wait();
     pdl_trigger();
-    constexpr int ROWS = ALIGNED ? 8 : 16, COLS = 64 / ROWS;
     const int64_t bn = blockIdx.x / nb, bk = blockIdx.x % nb;
-    const int t = threadIdx.x, lane = t & 31;
-    const int64_t r0 = bn * BLOCK + (ALIGNED ? t / 16 : t / 32);
-    const int64_t c0 = bk * BLOCK + (ALIGNED ? (t % 16) * 8 : lane);
-    constexpr int RSTEP = ALIGNED ? 16 : 8, CSTEP = ALIGNED ? 1 : 32;
-    float v[ROWS][COLS];
+    const int t = threadIdx.x;
+    const int64_t r0 = bn * BLOCK + t / 16, k = bk * BLOCK + (t % 16) * 8;
+    Raw8<T> v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + i * 16;
+        v[i] = r < n && k + 8 <= d ? load_raw8(w + r * ldw + k) : load_some8(w + r * ldw + k, r < n ? d - k : 0);
+    }
     uint32_t a = 0;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int64_t r = r0 + i * RSTEP;
-        if (ALIGNED && r < n && c0 + 8 <= d) {
-            if constexpr (ALIGNED) load8(w + r * ldw + c0, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < COLS; ++j) {
-                const int64_t c = c0 + j * CSTEP;
-                v[i][j] = r < n && c < d ? to_f32(w[r * ldw + c]) : 0.0f;
-            }
-        }
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = top8(v[i]);
+        a = sizeof(T) == 4 ? max(a, b) : __vmaxu2(a, b);
     }
+    if (sizeof(T) != 4) a = max(a & 0xFFFFu, a >> 16);
+    a = __reduce_max_sync(0xFFFFFFFFu, a);
+    if ((t & 31) == 0) part[t / 32] = a;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
+    for (int i = 0; i < 8; ++i) a = max(a, part[i]);
+    a = top_bits<T>(a);
+    const float scale = block_scale(a);
+    if (t == 0) {
+        scales[bn * nb + bk] = scale;
+        if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(bn * BLOCK));
+    }
+    const Scale c(scale);
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) a = max(a, abs_bits(v[i][j]));
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + i * 16;
+        if (r >= n || k >= d) break;
+        float f[8];
+        widen8(v[i], f);
+        store8(codes + r * ldc + k, codes8(f, c), d - k);
+    }
+}
+
+// The same at any alignment: columns lane, lane + 32, ... of every eighth row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    quant_weight_any_kernel(const T* __restrict__ w, int64_t n, int64_t d, int64_t ldw, uint8_t* __restrict__ codes,
+                            int64_t ldc, float* __restrict__ scales, int nb, DevStatus* st) {
+    __shared__ uint32_t part[8];
+    pdl_wait();
+    pdl_trigger();
+    const int64_t bn = blockIdx.x / nb, bk = blockIdx.x % nb;
+    const int t = threadIdx.x, lane = t & 31;
+    const int64_t r0 = bn * BLOCK + t / 32, c0 = bk * BLOCK + lane;
+    float v[16][4];
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t r = r0 + i * 8, c = c0 + j * 32;
+            v[i][j] = r < n && c < d ? to_f32(w[r * ldw + c]) : 0.0f;
+            a = max(a, abs_bits(v[i][j]));
+        }
     a = __reduce_max_sync(0xFFFFFFFFu, a);
     if (lane == 0) part[t / 32] = a;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = max(a, part[i]);
-    float s = block_scale(a);
+    const float scale = block_scale(a);
     if (t == 0) {
-        scales[bn * nb + bk] = s;
+        scales[bn * nb + bk] = scale;
         if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(bn * BLOCK));
     }
-    const bool small = s < SMALL_SCALE;
-    if (small) s *= SMALL_LIFT;
-    const float y = __frcp_rn(s);
+    const Scale sc(scale);
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int64_t r = r0 + i * RSTEP;
+    for (int i = 0; i < 16; ++i) {
+        const int64_t r = r0 + i * 8;
         if (r >= n) break;
-        if (small) {
+        if (sc.small) {
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) v[i][j] *= SMALL_LIFT;
+            for (int j = 0; j < 4; ++j) v[i][j] *= SMALL_LIFT;
         }
+        const uint32_t c = codes4(v[i], sc.s, sc.y);
         uint8_t* out = codes + r * ldc + c0;
-        if constexpr (ALIGNED) {
-            const uint2 c = make_uint2(codes4(v[i], s, y), codes4(v[i] + 4, s, y));
-            if (c0 + 8 <= d) {
-                *reinterpret_cast<uint2*>(out) = c;
-            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c0 + j < d) out[j] = uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
-            }
-        } else {
-            const uint32_t c = codes4(v[i], s, y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c0 + 32 * j < d) out[32 * j] = uint8_t(c >> (8 * j));
-        }
+        for (int j = 0; j < 4; ++j)
+            if (c0 + 32 * j < d) out[32 * j] = uint8_t(c >> (8 * j));
     }
 }
 
@@ -227,7 +284,7 @@ int weight_of(const void* w, int64_t n, int64_t d, int64_t ldw, uint8_t* codes, 
     using namespace fp8;
     const int nb = int((d + BLOCK - 1) / BLOCK);
     const dim3 grid(unsigned((n + BLOCK - 1) / BLOCK * nb));
-    auto kernel = aligned_for<T>(w, ldw, codes) ? quant_weight_kernel<T, true> : quant_weight_kernel<T, false>;
+    auto kernel = aligned_for<T>(w, ldw, codes) ? quant_weight_kernel<T> : quant_weight_any_kernel<T>;
     if (launch_pdl(kernel, grid, dim3(256), 0, stream, static_cast<const T*>(w), n, d, ldw, codes, ldc, scales, nb,
                    st) != cudaSuccess)
         return GPTQ_ERR_CUDA;

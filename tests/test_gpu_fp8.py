@@ -117,6 +117,14 @@ def test_borders():
     check_rows(x, *quantized_rows(x))
 
 
+def test_every_scale():
+    """The scale is the correctly rounded amax / 448 for every significand."""
+    x = (torch.arange(1 << 23, dtype=torch.int32, device="cuda") + 0x3F800000).view(torch.float32)[:, None]
+    c, s = quantized_rows(x)
+    assert torch.equal(s[0], x[:, 0] / torch.full_like(x[:, 0], 448.0))
+    assert (c.float() == 448).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_nonfinite_block(bad):
     x = rand(4, 300, 1)
