@@ -36,43 +36,74 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Codes of the real quotients x / s, rounded once.
+// Two fp32 values in one 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Codes of the real quotients x / s, rounded once, without a division or a
+// branch.
 //
-// q = x y with y = rcp_approx(s) is within three units in the last place of
-// x / s (2^-23 of y's error, 2^-24 of the product's), so it rounds to the same
-// code unless a middle of two codes lies that near.  Middles have at most five
-// significant bits: q is near one when adding 4 leaves bits 3 .. 18 zero.
-// For 16-bit x that is common -- s is the rounded 1 / 448 of one of them, so
-// x / s sits just beside a middle whenever 448 x / amax is one, about one value in
-// 250 -- and rounding x / s to fp32 first would be as wrong as q.  Such a q is
-// replaced by its middle t moved by the remainder x - t s (exact in one fused
-// multiply-add: 29 bits of t s against at most 24 of x).  256 times the
-// remainder is at least 2^-21 of t if it is not zero, and at most 2^-13, far
-// from the next middle (2^-5): the code is the nearer one, and an exact middle
-// goes to the even one.  Needs x and s far enough above 2^-126 (SMALL_SCALE).
-__device__ __forceinline__ bool near_middle(float q) { return ((__float_as_uint(q) + 4u) & 0x7FFF8u) == 0u; }
-__device__ __forceinline__ float settle(float q, float x, float s, float y) {
-    const float t = __uint_as_float((__float_as_uint(q) + 4u) & ~7u);
-    const float r = __fmaf_rn(-t, s, x);
-    return near_middle(q) ? copysignf(__fmaf_rn(r, 256.0f * y, t), x) : q;   // -0 stays -0
-}
-__device__ __forceinline__ uint32_t code1(float x, float s, float y) {
-    return e4m3x2(settle(__fmul_rn(x, y), x, s, y), 0.0f);
-}
-__device__ __forceinline__ uint32_t codes4(const float* v, float s, float y) {
-    float q[4];
-    bool near = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        q[i] = __fmul_rn(v[i], y);
-        near |= near_middle(q[i]);
+// Rounding x y, y = rcp_approx(s), or even RN(x / s), can go wrong where the
+// quotient lies beside the middle of two codes, and for 16-bit x that is
+// common: s is the rounded 1 / 448 of one of them, so x / s is just beside a
+// middle whenever 448 x / amax is one, about one value in 250.  Codes have four
+// significant bits and middles five, so:
+//   h = x y rounded to five bits (Veltkamp's splitting: c = (2^19 + 1) q,
+//       h = c - (c - q)), the five-bit number nearest x / s up to an error far
+//       below half their spacing;
+//   r = x - h s in one fused multiply-add, whose sign is exact.
+// If h is a code, it is the answer, and if it is a middle, the sign of r
+// decides, or the even code where r = 0.  Either way the answer is h moved by
+// 2^-15 towards r's sign and rounded to four bits: 2^-15 is one unit in the
+// last place of 448, and smaller than the spacing of five-bit numbers from
+// 2^-10, the smallest middle, up.  (Just below 2^-10 the move may end on that
+// middle, which rounds to the even 0 as it should.)  r y 2^40 saturated to
+// [-1/2, 1/2] is the sign: a remainder that is not zero is at least 2^-29 of h s
+// (29 bits of h s against 24 of x).  The sign of a zero code is x's.
+// Needs x and s far enough above 2^-126 (SMALL_SCALE).
+struct Coder {
+    uint64_t y, minus_s;
+    float sign_scale;
+    __device__ __forceinline__ Coder(float s, float r) : y(pack2(r, r)), minus_s(pack2(-s, -s)), sign_scale(0x1p40f * r) {}
+    // codes of the two values of x, the first in the low byte, sign bits to be set by the caller
+    __device__ __forceinline__ uint32_t two(uint64_t x) const {
+        const uint64_t minus1 = pack2(-1.0f, -1.0f);
+        const uint64_t q = mul2(x, y), c = mul2(q, pack2(0x1p19f + 1.0f, 0x1p19f + 1.0f));
+        const uint64_t h = fma2(fma2(q, minus1, c), minus1, c);
+        float ra, rb, a, b;
+        unpack2(fma2(h, minus_s, x), ra, rb);
+        asm("fma.rn.sat.f32 %0, %1, %2, 0f3F000000;" : "=f"(a) : "f"(ra), "f"(sign_scale));   // 0, 1/2 or 1
+        asm("fma.rn.sat.f32 %0, %1, %2, 0f3F000000;" : "=f"(b) : "f"(rb), "f"(sign_scale));
+        const uint64_t low = fma2(h, pack2(1.0f, 1.0f), pack2(-0x1p-15f, -0x1p-15f));
+        unpack2(fma2(pack2(a, b), pack2(0x1p-14f, 0x1p-14f), low), a, b);
+        return e4m3x2(a, b);
     }
-    if (near) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = settle(q[i], v[i], s, y);
+    __device__ __forceinline__ uint32_t four(const float* v) const {
+        const uint32_t signs = __byte_perm(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0073),
+                                           __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0073), 0x5410);
+        const uint32_t codes = two(pack2(v[0], v[1])) | (two(pack2(v[2], v[3])) << 16);
+        return (codes & 0x7F7F7F7Fu) | (signs & 0x80808080u);
     }
-    return e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
-}
+    __device__ __forceinline__ uint32_t one(float v) const {
+        return (two(pack2(v, v)) & 0x7Fu) | (__float_as_uint(v) >> 31 << 7);
+    }
+};
 
 // Blocks whose scale is below this take their values and scale times
 // SMALL_LIFT first, exactly, so that the remainders above are exact.

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                 }
                 if (row < g.n)
                     static_cast<uint8_t*>(g.y)[(tok0 + c) * g.ldy + row] =
-                        uint8_t(code1(v, s, rcp_approx(s)));
+                        uint8_t(Coder(s, rcp_approx(s)).one(v));
             }
         }
     }
@@ -368,16 +368,9 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, ui
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// a[0..1] += v[0..1] * s (one instruction).
-__device__ __forceinline__ void fma2(float* a, const uint32_t* v, float s) {
-    asm("{\n\t.reg .b64 x, y, z;\n\t"
-        "mov.b64 x, {%0, %1};\n\t"
-        "mov.b64 y, {%2, %3};\n\t"
-        "mov.b64 z, {%4, %4};\n\t"
-        "fma.rn.f32x2 x, y, z, x;\n\t"
-        "mov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(a[0]), "+f"(a[1])
-        : "r"(v[0]), "r"(v[1]), "f"(s));
+// a[0..1] += v[0..1] * s
+__device__ __forceinline__ void add_scaled2(float* a, const uint32_t* v, float s) {
+    unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(s, s), pack2(a[0], a[1])), a[0], a[1]);
 }
 // Arrive on an mbarrier of either CTA without publishing memory: for an
 // accumulator that has been read (its loads have returned) nothing else needs
@@ -619,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 16; i += 2)
-                        fma2(acc + 16 * j + i, v[j & 1] + i, j < STEPS / 2 ? s0 : s1);
+                        add_scaled2(acc + 16 * j + i, v[j & 1] + i, j < STEPS / 2 ? s0 : s1);
                 }
             }
             if (!GATED) {
@@ -654,12 +647,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < OC; ++c) acc[c] *= SMALL_LIFT;
             }
-            const float y = rcp_approx(s);
+            const Coder code(s, rcp_approx(s));
 #pragma unroll
             for (int c = 0; c < OC; c += 16)
                 *reinterpret_cast<uint4*>(out_buf + Stage<OC>::at(lane, c / 16)) =
-                    make_uint4(codes4(acc + c, s, y), codes4(acc + c + 4, s, y), codes4(acc + c + 8, s, y),
-                               codes4(acc + c + 12, s, y));
+                    make_uint4(code.four(acc + c), code.four(acc + c + 4), code.four(acc + c + 8), code.four(acc + c + 12));
             Stage<OC>::flush(out_buf, static_cast<uint8_t*>(g.y) + (tok - lane) * g.ldy + col, g.ldy,
                              int(max(int64_t(0), min(g.m - (tok - lane), int64_t(32)))),
                              int(max(int64_t(0), min(g.n - col, int64_t(OC)))), true, lane);

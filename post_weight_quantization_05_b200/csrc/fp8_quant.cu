@@ -19,23 +19,37 @@ constexpr int CHUNK = 256 * UNROLL;   // values of a row one warp takes
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// What a block's codes are made with.
-struct Scale {
-    float s, y;     // the scale and its reciprocal, both lifted for a small one
+// The codes of a block: its values and scale are lifted together where the scale is small.
+struct BlockCoder {
     bool small;
-    __device__ __forceinline__ explicit Scale(float scale) {
-        small = scale < SMALL_SCALE;
-        s = small ? scale * SMALL_LIFT : scale;
-        y = rcp_approx(s);
+    Coder code;
+    __device__ __forceinline__ explicit BlockCoder(float scale)
+        : small(scale < SMALL_SCALE),
+          code(small ? scale * SMALL_LIFT : scale, rcp_approx(small ? scale * SMALL_LIFT : scale)) {}
+    template <int N>
+    __device__ __forceinline__ void lift(float (&v)[N]) const {
+        if (small) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] *= SMALL_LIFT;
+        }
+    }
+    // four codes whose values' signs lie in bit 7 of each byte of `signs`
+    __device__ __forceinline__ uint32_t four(const float* v, uint32_t signs) const {
+        const uint32_t c = code.two(pack2(v[0], v[1])) | (code.two(pack2(v[2], v[3])) << 16);
+        return (c & 0x7F7F7F7Fu) | (signs & 0x80808080u);
+    }
+    template <typename T>
+    __device__ __forceinline__ uint2 eight(const Raw8<T>& raw) const {
+        float v[8];
+        widen8(raw, v);
+        lift(v);
+        if constexpr (sizeof(T) == 4)
+            return make_uint2(code.four(v), code.four(v + 4));
+        else   // the high bytes of the 16-bit values hold the signs
+            return make_uint2(four(v, __byte_perm(raw.w[0], raw.w[1], 0x7531)),
+                              four(v + 4, __byte_perm(raw.w[2], raw.w[3], 0x7531)));
     }
 };
-__device__ __forceinline__ uint2 codes8(float* v, const Scale& c) {
-    if (c.small) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= SMALL_LIFT;
-    }
-    return make_uint2(codes4(v, c.s, c.y), codes4(v + 4, c.s, c.y));
-}
 __device__ __forceinline__ void store8(uint8_t* out, uint2 c, int64_t n) {
     if (n >= 8) {
         *reinterpret_cast<uint2*>(out) = c;
@@ -104,11 +118,8 @@ __global__ void __launch_bounds__(32 * WARPS)
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         const int64_t k = k0 + u * 256;
-        const Scale c(__shfl_sync(0xFFFFFFFFu, scale, (lane & 16) + u));
-        if (k >= d) continue;
-        float f[8];
-        widen8(v[u], f);
-        store8(codes + row * ldc + k, codes8(f, c), d - k);
+        const BlockCoder c(__shfl_sync(0xFFFFFFFFu, scale, (lane & 16) + u));
+        if (k < d) store8(codes + row * ldc + k, c.eight(v[u]), d - k);
     }
 }
 
@@ -145,12 +156,9 @@ __global__ void __launch_bounds__(32 * WARPS)
             scales[(kb / BLOCK) * lds + row] = scale;
             if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(row));
         }
-        const Scale sc(scale);
-        if (sc.small) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[b][i] *= SMALL_LIFT;
-        }
-        const uint32_t c = codes4(v[b], sc.s, sc.y);
+        const BlockCoder coder(scale);
+        coder.lift(v[b]);
+        const uint32_t c = coder.code.four(v[b]);
         uint8_t* out = codes + row * ldc + kb + lane;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -194,14 +202,12 @@ __global__ void __launch_bounds__(256)
         scales[bn * nb + bk] = scale;
         if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(bn * BLOCK));
     }
-    const Scale c(scale);
+    const BlockCoder c(scale);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = r0 + i * 16;
         if (r >= n || k >= d) break;
-        float f[8];
-        widen8(v[i], f);
-        store8(codes + r * ldc + k, codes8(f, c), d - k);
+        store8(codes + r * ldc + k, c.eight(v[i]), d - k);
     }
 }
 
@@ -236,16 +242,13 @@ __global__ void __launch_bounds__(256)
         scales[bn * nb + bk] = scale;
         if (a >= INF_BITS) record_error(st, GPTQ_ERR_NONFINITE, int(bn * BLOCK));
     }
-    const Scale sc(scale);
+    const BlockCoder coder(scale);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int64_t r = r0 + i * 8;
         if (r >= n) break;
-        if (sc.small) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] *= SMALL_LIFT;
-        }
-        const uint32_t c = codes4(v[i], sc.s, sc.y);
+        coder.lift(v[i]);
+        const uint32_t c = coder.code.four(v[i]);
         uint8_t* out = codes + r * ldc + c0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)

@@ -117,6 +117,19 @@ def test_borders():
     check_rows(x, *quantized_rows(x))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_every_bf16_ratio(dtype):
+    """Every bf16 value down to 2^-20 of the block's largest, for every
+    significand of the largest: the quotients next to a middle among them."""
+    values = torch.cat([(1 + torch.arange(128) / 128) * 2.0 ** -e for e in range(1, 21)])
+    values = torch.cat([values, torch.zeros(-len(values) % 127)]).view(-1, 127)
+    values[:, 1::2] *= -1
+    tops = 1 + torch.arange(128) / 128
+    x = torch.cat([values.expand(128, -1, -1), tops[:, None, None].expand(-1, values.shape[0], 1)], 2)
+    x = x.reshape(128, -1).to(DTYPES[dtype]).cuda()
+    check_rows(x, *quantized_rows(x))
+
+
 def test_every_scale():
     """The scale is the correctly rounded amax / 448 for every significand."""
     x = (torch.arange(1 << 23, dtype=torch.int32, device="cuda") + 0x3F800000).view(torch.float32)[:, None]
