@@ -50,6 +50,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -90,7 +95,7 @@ struct Coder {
         unpack2(fma2(h, minus_s, x), ra, rb);
         asm("fma.rn.sat.f32 %0, %1, %2, 0f3F000000;" : "=f"(a) : "f"(ra), "f"(sign_scale));   // 0, 1/2 or 1
         asm("fma.rn.sat.f32 %0, %1, %2, 0f3F000000;" : "=f"(b) : "f"(rb), "f"(sign_scale));
-        const uint64_t low = fma2(h, pack2(1.0f, 1.0f), pack2(-0x1p-15f, -0x1p-15f));
+        const uint64_t low = add2(h, pack2(-0x1p-15f, -0x1p-15f));
         unpack2(fma2(pack2(a, b), pack2(0x1p-14f, 0x1p-14f), low), a, b);
         return e4m3x2(a, b);
     }
