@@ -66,6 +66,18 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
 // Wait for this thread's TMEM loads; the values pass through it so that no
 // use of them can be moved in front of the wait.
 template <int N>
@@ -114,6 +126,12 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, float v, int out)
         static_cast<__half*>(y)[at] = __float2half_rn(v);
 }
 
+// 4-byte asynchronous copy to shared memory; zero if !live (src is not read).
+__device__ __forceinline__ void copy4_async(float* dst, const float* src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 4 : 0)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Weights on the MMA's M side: a tile is 128 weight rows (one row of scale
 // blocks) by NT tokens, which keeps the tile full for one token as for 128.
@@ -123,18 +141,30 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, float v, int out)
 template <int NT, bool GATED>
 struct Narrow {
     static constexpr int ACC = GATED ? 2 : 1;
-    static constexpr int STAGE_BYTES = ACC * TILE_BYTES + NT * 128;
-    static constexpr int STAGES = GATED ? 3 : 4;
-    static constexpr int SLOTS = 4;                      // TMEM accumulators
-    static constexpr int COLS = SLOTS * ACC * NT;        // a power of two, 64 .. 512
-    static constexpr int THREADS = 192;                  // 4 warps of sums, 1 of loads, 1 of MMAs
-    static constexpr int RING = 2 * ACC * NT;            // floats of scales per warp
-    static constexpr size_t SMEM_BYTES =
-        1024 + size_t(STAGES) * STAGE_BYTES + (4 * RING + 4 * NT) * 4 + (2 * STAGES + 2 * SLOTS) * 8 + 16;
+    static constexpr int BLOCK_BYTES = ACC * TILE_BYTES + NT * 128;
+    // A stage is a group of blocks of k: the issuing thread's waits and its
+    // commit cost about 0.34 us a stage, its MMAs 0.012 us each, against the
+    // 0.37 us that one SM's share of HBM takes for a block (16 KB).
+    static constexpr int GROUP = 2;
+    static constexpr int STAGE_BYTES = GROUP * BLOCK_BYTES;
+    static constexpr int SUM_WARPS = 8;                   // two sets of four take every other stage
+    static constexpr int THREADS = 32 * (SUM_WARPS + 2);  // and a warp each for loads and MMAs
+    static constexpr int MAX_SPLIT = 8;                  // CTAs of a tile: a portable cluster
+    static constexpr int AHEAD = 2, RING = 4;            // stages of scales per warp, in flight and kept
+    static constexpr int ENTRY = GROUP * (NT + 4);       // floats of one: per block the tokens', then the weights'
+    static constexpr int OTHER_BYTES = (SUM_WARPS * RING * ENTRY + 4 * NT) * 4;
+    static constexpr int STAGES = (232448 - 1024 - OTHER_BYTES - 256) / STAGE_BYTES;
+    static constexpr int STAGE_COLS = GROUP * ACC * NT;  // TMEM columns: an accumulator per block of the stage
+    static constexpr int COLS = STAGES * STAGE_COLS <= 64    ? 64
+                                : STAGES * STAGE_COLS <= 128 ? 128
+                                : STAGES * STAGE_COLS <= 256 ? 256
+                                                             : 512;
+    static constexpr int READ = STAGE_COLS < 64 ? STAGE_COLS : 64;   // accumulator columns read at once
+    static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + OTHER_BYTES + 3 * STAGES * 8 + 16;
     // the sums that the cluster exchanges, and the gated values, reuse the stages
-    static_assert((ACC * NT + (GATED ? NT : 0)) * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
+    static_assert((2 * ACC * NT + (GATED ? NT : 0)) * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
-    static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0, "TMEM columns");
+    static_assert(STAGES * STAGE_COLS <= 512, "TMEM columns");
 };
 
 template <int NT, bool GATED, int ACT>
@@ -144,13 +174,12 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     constexpr int ACC = C::ACC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* ring_all = reinterpret_cast<float*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);   // [4][2][ACC * NT]
-    uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + 4 * C::RING);                    // [NT][4]
+    float* ring_all = reinterpret_cast<float*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);   // [SUM_WARPS][RING][ENTRY]
+    uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + C::SUM_WARPS * C::RING * C::ENTRY);   // [NT][4]
     uint64_t* full = reinterpret_cast<uint64_t*>(amax + 4 * NT);   // [STAGES] TMA landed
-    uint64_t* empty = full + C::STAGES;                            // [STAGES] MMAs done with the stage
-    uint64_t* tfull = empty + C::STAGES;                           // [SLOTS] accumulator complete
-    uint64_t* tempty = tfull + C::SLOTS;                           // [SLOTS] accumulator read by four warps
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + C::SLOTS);
+    uint64_t* done = full + C::STAGES;                             // [STAGES] MMAs complete
+    uint64_t* read = done + C::STAGES;                             // [STAGES] accumulators read by four warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(read + C::STAGES);
 
     uint32_t split;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
@@ -158,7 +187,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = int(blockIdx.x / split);
     const int64_t row0 = int64_t(tile) * 128, tok0 = int64_t(blockIdx.y) * NT;
-    const int b0 = int(int64_t(g.nkb) * rank / split), b1 = int(int64_t(g.nkb) * (rank + 1) / split);
+    const int b0 = int(int64_t(g.nkb) * rank / split), blocks = int(int64_t(g.nkb) * (rank + 1) / split) - b0;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&maps.w);
@@ -166,11 +195,8 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
         tma_prefetch_desc(&maps.x);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int s = 0; s < C::SLOTS; ++s) {
-            mbar_init(&tfull[s], 1);
-            mbar_init(&tempty[s], 4);
+            mbar_init(&done[s], 1);
+            mbar_init(&read[s], 4);
         }
         fence_mbar_init();
     }
@@ -189,84 +215,102 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
 #pragma unroll
     for (int c = 0; c < ACC * NT; ++c) acc[c] = 0.0f;
 
-    if (warp == 4) {
+    const int groups = (blocks + C::GROUP - 1) / C::GROUP;
+    if (warp == C::SUM_WARPS) {
         if (lane == 0) {
-            for (int b = b0; b < b1; ++b) {
-                const int i = b - b0, s = i % C::STAGES;
-                if (!mbar_wait(&empty[s], (uint32_t(i / C::STAGES) & 1u) ^ 1u, g.st, 401)) break;
-                uint8_t* base = smem + size_t(s) * C::STAGE_BYTES;
-                mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
-                tma_load_2d(base, &maps.w, b * 128, int(row0), &full[s]);
-                if (GATED) tma_load_2d(base + TILE_BYTES, &maps.u, b * 128, int(row0), &full[s]);
-                tma_load_2d(base + ACC * TILE_BYTES, &maps.x, b * 128, int(tok0), &full[s]);
+            for (int i = 0; i < groups; ++i) {
+                const int s = i % C::STAGES, count = min(C::GROUP, blocks - i * C::GROUP);
+                if (!mbar_wait(&done[s], (uint32_t(i / C::STAGES) & 1u) ^ 1u, g.st, 401)) break;
+                mbar_arrive_expect_tx(&full[s], uint32_t(count) * C::BLOCK_BYTES);
+                for (int q = 0; q < count; ++q) {
+                    uint8_t* base = smem + size_t(s) * C::STAGE_BYTES + q * C::BLOCK_BYTES;
+                    const int k = (b0 + i * C::GROUP + q) * 128;
+                    tma_load_2d(base, &maps.w, k, int(row0), &full[s]);
+                    if (GATED) tma_load_2d(base + TILE_BYTES, &maps.u, k, int(row0), &full[s]);
+                    tma_load_2d(base + ACC * TILE_BYTES, &maps.x, k, int(tok0), &full[s]);
+                }
             }
         }
-    } else if (warp == 5) {
+    } else if (warp > C::SUM_WARPS) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_e4m3(128, NT);
-            for (int b = b0; b < b1; ++b) {
-                const int i = b - b0, s = i % C::STAGES, d = i % C::SLOTS;
-                if (!mbar_wait(&tempty[d], (uint32_t(i / C::SLOTS) & 1u) ^ 1u, g.st, 402)) break;
-                if (!mbar_wait(&full[s], uint32_t(i / C::STAGES) & 1u, g.st, 403)) break;
+            for (int i = 0; i < groups; ++i) {
+                const int s = i % C::STAGES, count = min(C::GROUP, blocks - i * C::GROUP);
+                const uint32_t round = uint32_t(i / C::STAGES) & 1u;
+                if (!mbar_wait(&read[s], round ^ 1u, g.st, 402)) break;
+                if (!mbar_wait(&full[s], round, g.st, 403)) break;
                 tc_fence_after();
-                const uint32_t wa = smem_u32(smem + size_t(s) * C::STAGE_BYTES), xa = wa + ACC * TILE_BYTES;
-                const uint32_t dt = tmem_base + uint32_t(d * ACC * NT);
 #pragma unroll
-                for (int a = 0; a < ACC; ++a)
+                for (int q = 0; q < C::GROUP; ++q) {
+                    if (q >= count) continue;
+                    const uint32_t wa = smem_u32(smem + size_t(s) * C::STAGE_BYTES + q * C::BLOCK_BYTES);
+                    const uint32_t xa = wa + ACC * TILE_BYTES;
+                    const uint32_t dt = tmem_base + uint32_t(s * C::STAGE_COLS + q * ACC * NT);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)   // 32 codes (32 bytes) of the 128-byte swizzle row
-                        umma_f8(dt + a * NT, sdesc_sw128(wa + a * TILE_BYTES + kk * 32, 16, 1024),
-                                sdesc_sw128(xa + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-                umma_commit(&empty[s]);
-                umma_commit(&tfull[d]);
+                    for (int a = 0; a < ACC; ++a)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)   // 32 codes (32 bytes) of the 128-byte swizzle row
+                            umma_f8(dt + a * NT, sdesc_sw128(wa + a * TILE_BYTES + kk * 32, 16, 1024),
+                                    sdesc_sw128(xa + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&done[s]);               // frees the stage and completes its accumulators
             }
         }
     } else {
         // ---------------- sums: thread = weight row (TMEM lane), registers = tokens
-        float* ring = ring_all + warp * C::RING;
-        constexpr int PER = (NT + 31) / 32;
-        float sx[PER], sw[ACC];
-        auto fetch = [&](int b) {
+        const int set = warp >> 2;
+        float* ring = ring_all + warp * C::RING * C::ENTRY;
+        const float* xs = g.xs + int64_t(b0) * g.lds + tok0;
+        const float *ws = g.ws + int64_t(tile) * g.nkb + b0, *us = GATED ? g.us + int64_t(tile) * g.nkb + b0 : nullptr;
+        auto fetch = [&](int i) {
+            float* at = ring + ((i >> 1) % C::RING) * C::ENTRY;
 #pragma unroll
-            for (int p = 0; p < PER; ++p) {
-                const int64_t t = tok0 + lane + 32 * p;
-                sx[p] = lane + 32 * p < NT && t < g.m ? __ldg(g.xs + int64_t(b) * g.lds + t) : 0.0f;
+            for (int c = lane; c < C::GROUP * NT; c += 32) {
+                const int q = c / NT, t = c % NT, b = i * C::GROUP + q;
+                const bool live = b < blocks && tok0 + t < g.m;
+                copy4_async(at + q * (NT + 4) + t, live ? xs + int64_t(b) * g.lds + t : xs, live);
             }
-            sw[0] = __ldg(g.ws + int64_t(tile) * g.nkb + b);
-            if (GATED) sw[ACC - 1] = __ldg(g.us + int64_t(tile) * g.nkb + b);
+            if (lane < C::GROUP * ACC) {
+                const int q = lane / ACC, a = lane % ACC, b = min(i * C::GROUP + q, blocks - 1);
+                copy4_async(at + q * (NT + 4) + NT + a, (GATED && a == 1 ? us : ws) + b, true);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        fetch(b0);
-        for (int b = b0; b < b1; ++b) {
-            const int i = b - b0, d = i % C::SLOTS;
-            float* mine = ring + (i & 1) * ACC * NT;
-#pragma unroll
-            for (int a = 0; a < ACC; ++a)
-#pragma unroll
-                for (int p = 0; p < PER; ++p)
-                    if (lane + 32 * p < NT) mine[a * NT + lane + 32 * p] = sx[p] * sw[a];
-            __syncwarp();
-            if (b + 1 < b1) fetch(b + 1);
-            const bool ok = mbar_wait(&tfull[d], uint32_t(i / C::SLOTS) & 1u, g.st, 404);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        for (int i = 0; i < C::AHEAD; ++i) fetch(2 * i + set);
+        bool live = true;    // a wait that ran out: go on without waiting
+        for (int i = set; i < groups; i += 2) {
+            const int s = i % C::STAGES, count = min(C::GROUP, blocks - i * C::GROUP);
+            fetch(i + 2 * C::AHEAD);
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
+            __syncwarp();                     // all lanes' copies of the stage's scales have landed
+            const float* scales = ring + ((i >> 1) % C::RING) * C::ENTRY;
+            if (live) live = mbar_wait(&done[s], uint32_t(i / C::STAGES) & 1u, g.st, 404);
+            live = __all_sync(0xFFFFFFFFu, live);
             tc_fence_after();
-            const uint32_t dt = tmem_base + (uint32_t(warp * 32) << 16) + uint32_t(d * ACC * NT);
+            const uint32_t dt = tmem_base + (uint32_t((warp & 3) * 32) << 16) + uint32_t(s * C::STAGE_COLS);
 #pragma unroll
-            for (int j = 0; j < ACC * NT; j += 16) {
-                uint32_t v[16];
-                tmem_ld_x16(dt + j, v);
+            for (int j = 0; j < C::STAGE_COLS; j += C::READ) {
+                uint32_t v[C::READ];
+#pragma unroll
+                for (int c = 0; c < C::READ; c += 32) tmem_ld_x32(dt + j + c, v + c);
                 tmem_ld_done(v);
-                if (j + 16 == ACC * NT) {   // this warp has read the whole accumulator
+                if (j + C::READ == C::STAGE_COLS) {   // this warp has read the whole stage
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty[d]);
+                    if (lane == 0) mbar_arrive(&read[s]);
                 }
 #pragma unroll
-                for (int q = 0; q < 16; q += 4) {
-                    const float4 s = *reinterpret_cast<const float4*>(mine + j + q);
-                    acc[j + q] = fmaf(__uint_as_float(v[q]), s.x, acc[j + q]);
-                    acc[j + q + 1] = fmaf(__uint_as_float(v[q + 1]), s.y, acc[j + q + 1]);
-                    acc[j + q + 2] = fmaf(__uint_as_float(v[q + 2]), s.z, acc[j + q + 2]);
-                    acc[j + q + 3] = fmaf(__uint_as_float(v[q + 3]), s.w, acc[j + q + 3]);
+                for (int c = 0; c < C::READ; c += 4) {
+                    const int q = (j + c) / (ACC * NT), a = (j + c) / NT % ACC, t = (j + c) % NT;
+                    if (q >= count) continue;         // (blocks behind the last are not written)
+                    const float* at = scales + q * (NT + 4);
+                    const float4 sx = *reinterpret_cast<const float4*>(at + t);
+                    const float w = at[NT + a];
+                    float* sum = acc + a * NT + t;
+                    sum[0] = fmaf(__uint_as_float(v[c]) * sx.x, w, sum[0]);
+                    sum[1] = fmaf(__uint_as_float(v[c + 1]) * sx.y, w, sum[1]);
+                    sum[2] = fmaf(__uint_as_float(v[c + 2]) * sx.z, w, sum[2]);
+                    sum[3] = fmaf(__uint_as_float(v[c + 3]) * sx.w, w, sum[3]);
                 }
             }
         }
@@ -277,36 +321,40 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem_base, C::COLS);
 
-    float* part = reinterpret_cast<float*>(smem);   // [ACC * NT][128] this CTA's sums
-    if (warp < 4) {
+    float* part = reinterpret_cast<float*>(smem);   // [2][ACC * NT][128] the sums of this CTA's two sets
+    const int set = warp >> 2, r = threadIdx.x & 127;
+    if (warp < C::SUM_WARPS) {
 #pragma unroll
-        for (int c = 0; c < ACC * NT; ++c) part[c * 128 + threadIdx.x] = acc[c];
+        for (int c = 0; c < ACC * NT; ++c) part[(set * ACC * NT + c) * 128 + r] = acc[c];
     }
     __syncwarp();
     cluster_sync();
     const int cols = int(min(int64_t(NT), g.m - tok0));
-    if (warp < 4) {
-        const int r = threadIdx.x;
+    if (warp < C::SUM_WARPS) {
+        // tokens (columns) rank, rank + split, ..., every other one to each set
+        const int first = int(rank) + set * int(split), step = 2 * int(split);
         const int64_t row = row0 + r;
-        float* held = part + ACC * NT * 128;        // gated values until their block's scale is known
-        for (int c = int(rank); c < cols; c += int(split)) {
+        float* held = part + 2 * ACC * NT * 128;    // gated values until their block's scale is known
+        for (int c = first; c < cols; c += step) {
             float v = 0.0f, u = 0.0f;
-            for (uint32_t q = 0; q < split; ++q) {
-                v += ld_cluster_f32(mapa_shared(part + c * 128 + r, q));
-                if (GATED) u += ld_cluster_f32(mapa_shared(part + (NT + c) * 128 + r, q));
-            }
+            for (uint32_t q = 0; q < split; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v += ld_cluster_f32(mapa_shared(part + (h * ACC * NT + c) * 128 + r, q));
+                    if (GATED) u += ld_cluster_f32(mapa_shared(part + (h * ACC * NT + NT + c) * 128 + r, q));
+                }
             if (GATED) v = gate_act<ACT>(v) * u;
             if (GATED && g.out == OUT_CODES) {
                 held[c * 128 + r] = v;
                 const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
-                if (lane == 0) amax[c * 4 + warp] = top;
+                if (lane == 0) amax[c * 4 + (warp & 3)] = top;
             } else if (row < g.n) {
                 store_out(g.y, (tok0 + c) * g.ldy + row, v, g.out);
             }
         }
         if (GATED && g.out == OUT_CODES) {
-            named_barrier_sync(1, 128);
-            for (int c = int(rank); c < cols; c += int(split)) {
+            named_barrier_sync(1 + set, 128);
+            for (int c = first; c < cols; c += step) {
                 const uint32_t a = max(max(amax[4 * c], amax[4 * c + 1]), max(amax[4 * c + 2], amax[4 * c + 3]));
                 float s = block_scale(a), v = held[c * 128 + r];
                 if (r == 0) {
@@ -318,8 +366,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                     v *= SMALL_LIFT;
                 }
                 if (row < g.n)
-                    static_cast<uint8_t*>(g.y)[(tok0 + c) * g.ldy + row] =
-                        uint8_t(Coder(s, rcp_approx(s)).one(v));
+                    static_cast<uint8_t*>(g.y)[(tok0 + c) * g.ldy + row] = uint8_t(Coder(s, rcp_approx(s)).one(v));
             }
         }
     }
@@ -380,12 +427,6 @@ __device__ __forceinline__ void add_scaled2(float* a, const uint32_t* v, float s
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// 4-byte asynchronous copy to shared memory; zero if !live (src is not read).
-__device__ __forceinline__ void copy4_async(float* dst, const float* src, bool live) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 4 : 0)
-                 : "memory");
-}
-
 // Tile t of tiles_m x tiles_n, in groups of eight tile rows: the tiles that run
 // at the same time share few token and weight rows, which L2 then serves.
 __device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm,
@@ -698,41 +739,49 @@ template <int NT, bool GATED, int ACT = 0>
 int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
     using C = fp8::Narrow<NT, GATED>;
     auto kernel = fp8::narrow_kernel<NT, GATED, ACT>;
-    static std::atomic<int> per_sm[kMaxDev];
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || sm_count(dev, &sms)) return GPTQ_ERR_CUDA;
-    if (per_sm[dev].load() == 0) {
-        int n = 0;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM_BYTES)) !=
-                cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, C::THREADS, C::SMEM_BYTES) != cudaSuccess)
-            return GPTQ_ERR_CUDA;
-        per_sm[dev].store(std::max(1, n));
-    }
+    static std::atomic<int> resident[kMaxDev][C::MAX_SPLIT + 1];   // clusters of 1 .. MAX_SPLIT CTAs the GPU holds at once
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return GPTQ_ERR_CUDA;
     fp8::Maps maps;
     std::memset(&maps, 0, sizeof(maps));
     int rc = make_code_map(encode, &maps.w, p.w, p.n, p.d, p.ldw, 128);
     if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, 128);
     if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, NT);
     if (rc) return rc;
-    fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, st};
-    // As many CTAs per tile as fill the GPU once, up to a portable cluster.
+    const fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, st};
     const int64_t rows = (p.n + 127) / 128, toks = (p.m + NT - 1) / NT;
-    const int64_t split = std::max<int64_t>(
-        1, std::min<int64_t>(std::min<int64_t>(8, g.nkb), int64_t(sms) * per_sm[dev].load() / (rows * toks)));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(rows * split), unsigned(toks));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(split);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    if (resident[dev][1].load() == 0) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM_BYTES)) !=
+            cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        for (int s = C::MAX_SPLIT; s >= 1; --s) {
+            int n = 0;
+            attr[0].val.clusterDim.x = unsigned(s);
+            cfg.gridDim = dim3(unsigned(s));
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return GPTQ_ERR_CUDA;
+            resident[dev][s].store(std::max(1, n));
+        }
+    }
+    // CTAs per tile: the most whose clusters all run at once (a cluster stays
+    // inside one GPC, so that is less than the CTAs that fit).  8192 x 28672, one
+    // token: 64 clusters of 6 take 39 us, of 2 46 us, of 7 (too many) 47 us.
+    int split = int(std::min<int64_t>(C::MAX_SPLIT, g.nkb));
+    while (split > 1 && rows * toks > resident[dev][split].load()) --split;
+    cfg.gridDim = dim3(unsigned(rows * split), unsigned(toks));
+    attr[0].val.clusterDim.x = unsigned(split);
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, maps, g) != cudaSuccess) return GPTQ_ERR_CUDA;
     count_launch();
@@ -776,7 +825,7 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
 
 // Tokens from which a product runs on SM pairs.  A build-time tuning knob.
 #ifndef GPTQ_FP8_WIDE_MIN_M
-#define GPTQ_FP8_WIDE_MIN_M 129
+#define GPTQ_FP8_WIDE_MIN_M 33
 #endif
 
 }  // namespace
@@ -785,8 +834,7 @@ template <int ACT>
 static int launch_gated(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
     if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<true, ACT>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, true, ACT>(p, stream, st, encode);
-    if (p.m <= 32) return launch_narrow<32, true, ACT>(p, stream, st, encode);
-    return launch_narrow<64, true, ACT>(p, stream, st, encode);
+    return launch_narrow<32, true, ACT>(p, stream, st, encode);
 }
 
 int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
@@ -795,9 +843,7 @@ int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, 
                                   : launch_gated<fp8::GELU>(p, stream, st, encode);
     if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<false>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, false>(p, stream, st, encode);
-    if (p.m <= 32) return launch_narrow<32, false>(p, stream, st, encode);
-    if (p.m <= 64) return launch_narrow<64, false>(p, stream, st, encode);
-    return launch_narrow<128, false>(p, stream, st, encode);
+    return launch_narrow<32, false>(p, stream, st, encode);
 }
 
 }  // namespace gptq
