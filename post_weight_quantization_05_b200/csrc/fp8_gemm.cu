@@ -134,18 +134,18 @@ __device__ __forceinline__ void copy4_async(float* dst, const float* src, bool l
 
 // ---------------------------------------------------------------------------
 // Weights on the MMA's M side: a tile is 128 weight rows (one row of scale
-// blocks) by NT tokens, which keeps the tile full for one token as for 128.
-// The cluster's CTAs share a tile's blocks of k and add their sums through
+// blocks) by NT tokens, which keeps the tile full for one token as for 32.
+// The cluster's CTAs share a tile's blocks of k -- a gated pair's even ones the
+// gate's, the odd ones the up projection's -- and add their sums through
 // distributed shared memory in rank order: no workspace, no atomics, the same
 // bits on every call.
-template <int NT, bool GATED>
+template <int NT>
 struct Narrow {
-    static constexpr int ACC = GATED ? 2 : 1;
-    static constexpr int BLOCK_BYTES = ACC * TILE_BYTES + NT * 128;
+    static constexpr int BLOCK_BYTES = TILE_BYTES + NT * 128;
     // A stage is a group of blocks of k: the issuing thread's waits and its
     // commit cost about 0.34 us a stage, its MMAs 0.012 us each, against the
     // 0.37 us that one SM's share of HBM takes for a block (16 KB).
-    static constexpr int GROUP = 2;
+    static constexpr int GROUP = NT <= 64 ? 2 : 1;
     static constexpr int STAGE_BYTES = GROUP * BLOCK_BYTES;
     static constexpr int SUM_WARPS = 8;                   // two sets of four take every other stage
     static constexpr int THREADS = 32 * (SUM_WARPS + 2);  // and a warp each for loads and MMAs
@@ -153,25 +153,30 @@ struct Narrow {
     static constexpr int AHEAD = 2, RING = 4;            // stages of scales per warp, in flight and kept
     static constexpr int ENTRY = GROUP * (NT + 4);       // floats of one: per block the tokens', then the weights'
     static constexpr int OTHER_BYTES = (SUM_WARPS * RING * ENTRY + 4 * NT) * 4;
-    static constexpr int STAGES = (232448 - 1024 - OTHER_BYTES - 256) / STAGE_BYTES;
-    static constexpr int STAGE_COLS = GROUP * ACC * NT;  // TMEM columns: an accumulator per block of the stage
+    // One CTA or two per SM share its 228 KB (1 KB of them per CTA the driver's).
+    // Two for up to 16 tokens leave fewer SMs idle: 11008 x 4096, 8 tokens 11.3 us
+    // against 13.7 with one; for 32 they would have too few stages.
+    static constexpr int PER_SM = NT <= 32 ? 2 : 1;
+    static constexpr int FIT = (233472 / PER_SM - 1024 - 1024 - OTHER_BYTES - 256) / STAGE_BYTES;
+    static constexpr int STAGES = FIT * GROUP * NT <= 512 ? FIT : 512 / (GROUP * NT);
+    static constexpr int STAGE_COLS = GROUP * NT;  // TMEM columns: an accumulator per block of the stage
     static constexpr int COLS = STAGES * STAGE_COLS <= 64    ? 64
                                 : STAGES * STAGE_COLS <= 128 ? 128
                                 : STAGES * STAGE_COLS <= 256 ? 256
                                                              : 512;
-    static constexpr int READ = STAGE_COLS < 64 ? STAGE_COLS : 64;   // accumulator columns read at once
+    static constexpr int READ = 32;                      // accumulator columns read at once
     static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + OTHER_BYTES + 3 * STAGES * 8 + 16;
     // the sums that the cluster exchanges, and the gated values, reuse the stages
-    static_assert((2 * ACC * NT + (GATED ? NT : 0)) * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
+    static_assert((NT <= 64 ? 3 : 2) * NT * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
-    static_assert(STAGES * STAGE_COLS <= 512, "TMEM columns");
+    static_assert(PER_SM * COLS <= 512 && STAGES * STAGE_COLS <= COLS, "TMEM columns");
+    static_assert(STAGES >= 2, "a set of sum warps starts a stage's second round after the other's first");
 };
 
 template <int NT, bool GATED, int ACT>
-__global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
+__global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
     narrow_kernel(const __grid_constant__ Maps maps, const Args g) {
-    using C = Narrow<NT, GATED>;
-    constexpr int ACC = C::ACC;
+    using C = Narrow<NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* ring_all = reinterpret_cast<float*>(smem + size_t(C::STAGES) * C::STAGE_BYTES);   // [SUM_WARPS][RING][ENTRY]
@@ -187,11 +192,14 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = int(blockIdx.x / split);
     const int64_t row0 = int64_t(tile) * 128, tok0 = int64_t(blockIdx.y) * NT;
-    const int b0 = int(int64_t(g.nkb) * rank / split), blocks = int(int64_t(g.nkb) * (rank + 1) / split) - b0;
+    // this CTA's weight and its blocks of k
+    const bool up = GATED && (rank & 1u);
+    const uint32_t share = GATED ? rank >> 1 : rank, shares = GATED ? split >> 1 : split;
+    const int b0 = int(int64_t(g.nkb) * share / shares), blocks = int(int64_t(g.nkb) * (share + 1) / shares) - b0;
+    const CUtensorMap* wmap = up ? &maps.u : &maps.w;
 
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&maps.w);
-        if (GATED) tma_prefetch_desc(&maps.u);
+        tma_prefetch_desc(wmap);
         tma_prefetch_desc(&maps.x);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -211,9 +219,9 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    float acc[ACC * NT];
+    float acc[NT];
 #pragma unroll
-    for (int c = 0; c < ACC * NT; ++c) acc[c] = 0.0f;
+    for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
 
     const int groups = (blocks + C::GROUP - 1) / C::GROUP;
     if (warp == C::SUM_WARPS) {
@@ -225,9 +233,8 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                 for (int q = 0; q < count; ++q) {
                     uint8_t* base = smem + size_t(s) * C::STAGE_BYTES + q * C::BLOCK_BYTES;
                     const int k = (b0 + i * C::GROUP + q) * 128;
-                    tma_load_2d(base, &maps.w, k, int(row0), &full[s]);
-                    if (GATED) tma_load_2d(base + TILE_BYTES, &maps.u, k, int(row0), &full[s]);
-                    tma_load_2d(base + ACC * TILE_BYTES, &maps.x, k, int(tok0), &full[s]);
+                    tma_load_2d(base, wmap, k, int(row0), &full[s]);
+                    tma_load_2d(base + TILE_BYTES, &maps.x, k, int(tok0), &full[s]);
                 }
             }
         }
@@ -244,14 +251,12 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                 for (int q = 0; q < C::GROUP; ++q) {
                     if (q >= count) continue;
                     const uint32_t wa = smem_u32(smem + size_t(s) * C::STAGE_BYTES + q * C::BLOCK_BYTES);
-                    const uint32_t xa = wa + ACC * TILE_BYTES;
-                    const uint32_t dt = tmem_base + uint32_t(s * C::STAGE_COLS + q * ACC * NT);
+                    const uint32_t xa = wa + TILE_BYTES;
+                    const uint32_t dt = tmem_base + uint32_t(s * C::STAGE_COLS + q * NT);
 #pragma unroll
-                    for (int a = 0; a < ACC; ++a)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)   // 32 codes (32 bytes) of the 128-byte swizzle row
-                            umma_f8(dt + a * NT, sdesc_sw128(wa + a * TILE_BYTES + kk * 32, 16, 1024),
-                                    sdesc_sw128(xa + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk)   // 32 codes (32 bytes) of the 128-byte swizzle row
+                        umma_f8(dt, sdesc_sw128(wa + kk * 32, 16, 1024), sdesc_sw128(xa + kk * 32, 16, 1024), idesc,
+                                kk > 0 ? 1u : 0u);
                 }
                 umma_commit(&done[s]);               // frees the stage and completes its accumulators
             }
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
         const int set = warp >> 2;
         float* ring = ring_all + warp * C::RING * C::ENTRY;
         const float* xs = g.xs + int64_t(b0) * g.lds + tok0;
-        const float *ws = g.ws + int64_t(tile) * g.nkb + b0, *us = GATED ? g.us + int64_t(tile) * g.nkb + b0 : nullptr;
+        const float* ws = (up ? g.us : g.ws) + int64_t(tile) * g.nkb + b0;
         auto fetch = [&](int i) {
             float* at = ring + ((i >> 1) % C::RING) * C::ENTRY;
 #pragma unroll
@@ -270,10 +275,7 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                 const bool live = b < blocks && tok0 + t < g.m;
                 copy4_async(at + q * (NT + 4) + t, live ? xs + int64_t(b) * g.lds + t : xs, live);
             }
-            if (lane < C::GROUP * ACC) {
-                const int q = lane / ACC, a = lane % ACC, b = min(i * C::GROUP + q, blocks - 1);
-                copy4_async(at + q * (NT + 4) + NT + a, (GATED && a == 1 ? us : ws) + b, true);
-            }
+            if (lane < C::GROUP) copy4_async(at + lane * (NT + 4) + NT, ws + min(i * C::GROUP + lane, blocks - 1), true);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         for (int i = 0; i < C::AHEAD; ++i) fetch(2 * i + set);
@@ -301,12 +303,12 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < C::READ; c += 4) {
-                    const int q = (j + c) / (ACC * NT), a = (j + c) / NT % ACC, t = (j + c) % NT;
+                    const int q = (j + c) / NT, t = (j + c) % NT;
                     if (q >= count) continue;         // (blocks behind the last are not written)
                     const float* at = scales + q * (NT + 4);
                     const float4 sx = *reinterpret_cast<const float4*>(at + t);
-                    const float w = at[NT + a];
-                    float* sum = acc + a * NT + t;
+                    const float w = at[NT];
+                    float* sum = acc + t;
                     sum[0] = fmaf(__uint_as_float(v[c]) * sx.x, w, sum[0]);
                     sum[1] = fmaf(__uint_as_float(v[c + 1]) * sx.y, w, sum[1]);
                     sum[2] = fmaf(__uint_as_float(v[c + 2]) * sx.z, w, sum[2]);
@@ -321,11 +323,11 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem_base, C::COLS);
 
-    float* part = reinterpret_cast<float*>(smem);   // [2][ACC * NT][128] the sums of this CTA's two sets
+    float* part = reinterpret_cast<float*>(smem);   // [2][NT][128] the sums of this CTA's two sets
     const int set = warp >> 2, r = threadIdx.x & 127;
     if (warp < C::SUM_WARPS) {
 #pragma unroll
-        for (int c = 0; c < ACC * NT; ++c) part[(set * ACC * NT + c) * 128 + r] = acc[c];
+        for (int c = 0; c < NT; ++c) part[(set * NT + c) * 128 + r] = acc[c];
     }
     __syncwarp();
     cluster_sync();
@@ -334,14 +336,17 @@ __global__ void __launch_bounds__(Narrow<NT, GATED>::THREADS, 1)
         // tokens (columns) rank, rank + split, ..., every other one to each set
         const int first = int(rank) + set * int(split), step = 2 * int(split);
         const int64_t row = row0 + r;
-        float* held = part + 2 * ACC * NT * 128;    // gated values until their block's scale is known
+        float* held = part + 2 * NT * 128;    // gated values until their block's scale is known
         for (int c = first; c < cols; c += step) {
             float v = 0.0f, u = 0.0f;
             for (uint32_t q = 0; q < split; ++q)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    v += ld_cluster_f32(mapa_shared(part + (h * ACC * NT + c) * 128 + r, q));
-                    if (GATED) u += ld_cluster_f32(mapa_shared(part + (h * ACC * NT + NT + c) * 128 + r, q));
+                    const float p = ld_cluster_f32(mapa_shared(part + (h * NT + c) * 128 + r, q));
+                    if (GATED && (q & 1u))
+                        u += p;
+                    else
+                        v += p;
                 }
             if (GATED) v = gate_act<ACT>(v) * u;
             if (GATED && g.out == OUT_CODES) {
@@ -737,7 +742,7 @@ int sm_count(int dev, int* out) {
 
 template <int NT, bool GATED, int ACT = 0>
 int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
-    using C = fp8::Narrow<NT, GATED>;
+    using C = fp8::Narrow<NT>;
     auto kernel = fp8::narrow_kernel<NT, GATED, ACT>;
     static std::atomic<int> resident[kMaxDev][C::MAX_SPLIT + 1];   // clusters of 1 .. MAX_SPLIT CTAs the GPU holds at once
     int dev = 0;
@@ -772,14 +777,15 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
             cfg.gridDim = dim3(unsigned(s));
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return GPTQ_ERR_CUDA;
-            resident[dev][s].store(std::max(1, n));
+            resident[dev][s].store(std::max(1, n * C::PER_SM));   // (the query counts one CTA that uses TMEM per SM)
         }
     }
     // CTAs per tile: the most whose clusters all run at once (a cluster stays
     // inside one GPC, so that is less than the CTAs that fit).  8192 x 28672, one
-    // token: 64 clusters of 6 take 39 us, of 2 46 us, of 7 (too many) 47 us.
-    int split = int(std::min<int64_t>(C::MAX_SPLIT, g.nkb));
-    while (split > 1 && rows * toks > resident[dev][split].load()) --split;
+    // token: 64 clusters of 4 take 38 us, of 2 47 us, of 5 (too many) 53 us.
+    constexpr int STEP = GATED ? 2 : 1;      // a gated pair's CTAs come in twos
+    int split = int(std::min<int64_t>(C::MAX_SPLIT, STEP * g.nkb));
+    while (split > STEP && rows * toks > resident[dev][split].load()) split -= STEP;
     cfg.gridDim = dim3(unsigned(rows * split), unsigned(toks));
     attr[0].val.clusterDim.x = unsigned(split);
     cfg.numAttrs = 2;
@@ -825,7 +831,7 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
 
 // Tokens from which a product runs on SM pairs.  A build-time tuning knob.
 #ifndef GPTQ_FP8_WIDE_MIN_M
-#define GPTQ_FP8_WIDE_MIN_M 33
+#define GPTQ_FP8_WIDE_MIN_M 129
 #endif
 
 }  // namespace
@@ -834,7 +840,8 @@ template <int ACT>
 static int launch_gated(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
     if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<true, ACT>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, true, ACT>(p, stream, st, encode);
-    return launch_narrow<32, true, ACT>(p, stream, st, encode);
+    if (p.m <= 32) return launch_narrow<32, true, ACT>(p, stream, st, encode);
+    return launch_narrow<64, true, ACT>(p, stream, st, encode);
 }
 
 int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
@@ -843,7 +850,9 @@ int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, 
                                   : launch_gated<fp8::GELU>(p, stream, st, encode);
     if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<false>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, false>(p, stream, st, encode);
-    return launch_narrow<32, false>(p, stream, st, encode);
+    if (p.m <= 32) return launch_narrow<32, false>(p, stream, st, encode);
+    if (p.m <= 64) return launch_narrow<64, false>(p, stream, st, encode);
+    return launch_narrow<128, false>(p, stream, st, encode);
 }
 
 }  // namespace gptq
