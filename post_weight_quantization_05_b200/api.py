@@ -258,38 +258,48 @@ _FP8_OUT = 3
 _ACTS = {"silu": 0, "gelu": 1}
 
 
-def _pitch(t, cols, name, step=1):
-    """Elements between the rows of a 2-D tensor with unit column stride (for
-    a single row any pitch will do: the next multiple of `step`)."""
-    if t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError(f"{name} must have {cols} columns, got {tuple(t.shape)}")
-    rs, cs = t.stride()
-    if cs != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return rs if t.shape[0] > 1 else -(-cols // step) * step
-
-
-def _typed(t, dtypes, rows, name, device):
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.shape[0] != rows:
-        raise ValueError(f"{name} must have {rows} rows, got {tuple(t.shape)}")
-
-
 _F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_I64 = (torch.int64,)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _rows(t, dtypes, shape, device, name, step=1):
+    """Check a 2-D tensor with unit column stride; its elements between rows
+    (for a single row any will do: the next multiple of `step`).  `device` is
+    an index.  These calls are made per layer and token, so the checks are few."""
+    if t.get_device() != device or t.dtype not in dtypes or t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} of {' or '.join(map(str, dtypes))} on cuda:{device}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    pitch, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return pitch if shape[0] > 1 else -(-shape[1] // step) * step
+
+
+def _dense(t, dtypes, shape, device, name):
+    if t.get_device() != device or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)} of {' or '.join(map(str, dtypes))} on "
+                         f"cuda:{device}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
+def _matrix(t, name):
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    return t.shape[0], t.shape[1], t.get_device()
 
 
 def _call(where, device, stream, *args):
-    """Call an entry point with `device` current and the stream last: the one
-    given, or the tensors' device's current one."""
+    """Call an entry point with the tensors' device current and the stream
+    last: the one given, or that device's current one."""
     fn = getattr(_lib(), where)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    raw = _raw_stream(device) if stream is None else stream.cuda_stream
+    if device == torch.cuda.current_device():
+        code = fn(*args, raw)
     else:
-        code = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+        with torch.cuda.device(device):
+            code = fn(*args, raw)
     if code:
         raise GPTQError(code, where)
 
@@ -309,53 +319,35 @@ def fp8_quantize_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
     """e4m3 codes of activations x [m, d_in] (fp32, bf16 or fp16; rows may be
     pitched) with a scale per token and 128 channels: codes [m, d_in] (float8_e4m3fn
     or uint8, 16-byte row pitch), scales [fp8_blocks(d_in), m] fp32."""
-    m, d = x.shape
-    dev = x.device
-    _typed(x, _VALUE_DTYPES, m, "x", dev)
-    _typed(codes, _CODE_DTYPES, m, "codes", dev)
-    _typed(scales, _F32, fp8_blocks(d), "scales", dev)
-    _call("gptq_fp8_quantize_rows", dev, stream, x.data_ptr(), _VALUE_DTYPES[x.dtype], m, d, _pitch(x, d, "x"),
-          codes.data_ptr(), _pitch(codes, d, "codes", 16), scales.data_ptr(), _pitch(scales, m, "scales"))
+    m, d, dev = _matrix(x, "x")
+    _call("gptq_fp8_quantize_rows", dev, stream, x.data_ptr(), _VALUE_DTYPES.get(x.dtype, -1), m, d,
+          _rows(x, _VALUE_DTYPES, (m, d), dev, "x"), codes.data_ptr(),
+          _rows(codes, _CODE_DTYPES, (m, d), dev, "codes", 16), scales.data_ptr(),
+          _rows(scales, _F32, (-(-d // 128), m), dev, "scales"))
 
 
 def fp8_quantize_weight(W: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
     """e4m3 codes of a weight W [d_out, d_in] with a scale per 128 x 128 block:
-    codes [d_out, d_in], scales [fp8_blocks(d_out), fp8_blocks(d_in)] fp32."""
-    n, d = W.shape
-    dev = W.device
-    _typed(W, _VALUE_DTYPES, n, "W", dev)
-    _typed(codes, _CODE_DTYPES, n, "codes", dev)
-    _weight_scales(scales, n, d, "scales", dev)
-    _call("gptq_fp8_quantize_weight", dev, stream, W.data_ptr(), _VALUE_DTYPES[W.dtype], n, d, _pitch(W, d, "W"),
-          codes.data_ptr(), _pitch(codes, d, "codes", 16), scales.data_ptr())
-
-
-def _weight_scales(scales, n, d, name, dev):
-    _typed(scales, _F32, fp8_blocks(n), name, dev)
-    if scales.shape[1] != fp8_blocks(d) or not scales.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [{fp8_blocks(n)}, {fp8_blocks(d)}]")
-
-
-def _fp8_operands(x, x_scales, w, w_scales, y):
-    m, d = x.shape
-    n = w.shape[0]
-    dev = x.device
-    _typed(x, _CODE_DTYPES, m, "x", dev)
-    _typed(x_scales, _F32, fp8_blocks(d), "x_scales", dev)
-    _typed(w, _CODE_DTYPES, n, "w", dev)
-    _weight_scales(w_scales, n, d, "w_scales", dev)
-    return m, n, d, dev
+    codes [d_out, d_in], scales [fp8_blocks(d_out), fp8_blocks(d_in)] fp32, contiguous."""
+    n, d, dev = _matrix(W, "W")
+    _dense(scales, _F32, (-(-n // 128), -(-d // 128)), dev, "scales")
+    _call("gptq_fp8_quantize_weight", dev, stream, W.data_ptr(), _VALUE_DTYPES.get(W.dtype, -1), n, d,
+          _rows(W, _VALUE_DTYPES, (n, d), dev, "W"), codes.data_ptr(),
+          _rows(codes, _CODE_DTYPES, (n, d), dev, "codes", 16), scales.data_ptr())
 
 
 def fp8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, y: torch.Tensor,
              stream=None):
     """y = x w^T from codes and scales (as the two calls above write them), y
     [m, d_out] fp32, bf16 or fp16; rows may be pitched."""
-    m, n, d, dev = _fp8_operands(x, x_scales, w, w_scales, y)
-    _typed(y, _VALUE_DTYPES, m, "y", dev)
-    _call("gptq_fp8_gemm", dev, stream, x.data_ptr(), _pitch(x, d, "x", 16), x_scales.data_ptr(),
-          _pitch(x_scales, m, "x_scales"), w.data_ptr(), _pitch(w, d, "w", 16), w_scales.data_ptr(), m, n, d,
-          _VALUE_DTYPES[y.dtype], y.data_ptr(), _pitch(y, n, "y"))
+    m, d, dev = _matrix(x, "x")
+    n = w.shape[0]
+    blocks = -(-d // 128)
+    _dense(w_scales, _F32, (-(-n // 128), blocks), dev, "w_scales")
+    _call("gptq_fp8_gemm", dev, stream, x.data_ptr(), _rows(x, _CODE_DTYPES, (m, d), dev, "x", 16),
+          x_scales.data_ptr(), _rows(x_scales, _F32, (blocks, m), dev, "x_scales"), w.data_ptr(),
+          _rows(w, _CODE_DTYPES, (n, d), dev, "w", 16), w_scales.data_ptr(), m, n, d, _VALUE_DTYPES.get(y.dtype, -1),
+          y.data_ptr(), _rows(y, _VALUE_DTYPES, (m, n), dev, "y"))
 
 
 def fp8_gated(x: torch.Tensor, x_scales: torch.Tensor, gate: torch.Tensor, gate_scales: torch.Tensor,
@@ -364,28 +356,29 @@ def fp8_gated(x: torch.Tensor, x_scales: torch.Tensor, gate: torch.Tensor, gate_
     """y = act(x gate^T) * (x up^T) in one kernel, act "silu" or "gelu": values
     (y fp32, bf16 or fp16), or codes (y float8_e4m3fn or uint8) with y_scales
     [fp8_blocks(d_out), m], ready for the next product."""
-    m, n, d, dev = _fp8_operands(x, x_scales, gate, gate_scales, y)
-    _typed(up, _CODE_DTYPES, n, "up", dev)
-    _weight_scales(up_scales, n, d, "up_scales", dev)
-    ldw = _pitch(gate, d, "gate", 16)
-    if _pitch(up, d, "up", 16) != ldw:
+    m, d, dev = _matrix(x, "x")
+    n = gate.shape[0]
+    blocks = -(-d // 128)
+    _dense(gate_scales, _F32, (-(-n // 128), blocks), dev, "gate_scales")
+    _dense(up_scales, _F32, (-(-n // 128), blocks), dev, "up_scales")
+    ldw = _rows(gate, _CODE_DTYPES, (n, d), dev, "gate", 16)
+    if _rows(up, _CODE_DTYPES, (n, d), dev, "up", 16) != ldw:
         raise ValueError("gate and up must have the same row pitch")
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     if y.dtype in _CODE_DTYPES:
-        _typed(y, _CODE_DTYPES, m, "y", dev)
         if y_scales is None:
             raise ValueError("codes need y_scales")
-        _typed(y_scales, _F32, fp8_blocks(n), "y_scales", dev)
-        out, ldy, ys, ldys = _FP8_OUT, _pitch(y, n, "y", 16), y_scales.data_ptr(), _pitch(y_scales, m, "y_scales")
+        out, ldy, ys = _FP8_OUT, _rows(y, _CODE_DTYPES, (m, n), dev, "y", 16), y_scales.data_ptr()
+        ldys = _rows(y_scales, _F32, (-(-n // 128), m), dev, "y_scales")
     else:
-        _typed(y, _VALUE_DTYPES, m, "y", dev)
         if y_scales is not None:
             raise ValueError("y_scales go with codes only")
-        out, ldy, ys, ldys = _VALUE_DTYPES[y.dtype], _pitch(y, n, "y"), None, 0
-    _call("gptq_fp8_gated", dev, stream, x.data_ptr(), _pitch(x, d, "x", 16), x_scales.data_ptr(),
-          _pitch(x_scales, m, "x_scales"), gate.data_ptr(), gate_scales.data_ptr(), up.data_ptr(),
-          up_scales.data_ptr(), ldw, m, n, d, _ACTS[act], out, y.data_ptr(), ldy, ys, ldys)
+        out, ldy, ys, ldys = _VALUE_DTYPES.get(y.dtype, -1), _rows(y, _VALUE_DTYPES, (m, n), dev, "y"), None, 0
+    _call("gptq_fp8_gated", dev, stream, x.data_ptr(), _rows(x, _CODE_DTYPES, (m, d), dev, "x", 16),
+          x_scales.data_ptr(), _rows(x_scales, _F32, (blocks, m), dev, "x_scales"), gate.data_ptr(),
+          gate_scales.data_ptr(), up.data_ptr(), up_scales.data_ptr(), ldw, m, n, d, _ACTS[act], out, y.data_ptr(),
+          ldy, ys, ldys)
 
 
 # ----------------------------------------------------------------- token scores
@@ -396,30 +389,22 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, logp: torch.Tens
     logp[i] = ln softmax(logits[i])[targets[i]] (0 where targets[i] < 0), the
     entropy, and, with top_logp and top_ids [n, k], the k <= 32 likeliest
     tokens (equal ones by increasing index).  targets int64."""
-    n, v = logits.shape
-    dev = logits.device
-    _typed(logits, _VALUE_DTYPES, n, "logits", dev)
-    _vector(targets, torch.int64, n, "targets", dev)
-    _vector(logp, torch.float32, n, "logp", dev)
+    n, v, dev = _matrix(logits, "logits")
+    _dense(targets, _I64, (n,), dev, "targets")
+    _dense(logp, _F32, (n,), dev, "logp")
     if entropy is not None:
-        _vector(entropy, torch.float32, n, "entropy", dev)
+        _dense(entropy, _F32, (n,), dev, "entropy")
     if (top_logp is None) != (top_ids is None):
         raise ValueError("top_logp and top_ids go together")
     k = 0
     if top_logp is not None:
         k = top_logp.shape[-1]
-        for t, dtype, name in ((top_logp, torch.float32, "top_logp"), (top_ids, torch.int32, "top_ids")):
-            if t.device != dev or t.dtype != dtype or t.shape != (n, k) or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous {dtype} [{n}, {k}] on the logits' device")
-    _call("gptq_token_logprobs", dev, stream, logits.data_ptr(), _VALUE_DTYPES[logits.dtype], n, v,
-          _pitch(logits, v, "logits"), targets.data_ptr(), logp.data_ptr(),
+        _dense(top_logp, _F32, (n, k), dev, "top_logp")
+        _dense(top_ids, _I32, (n, k), dev, "top_ids")
+    _call("gptq_token_logprobs", dev, stream, logits.data_ptr(), _VALUE_DTYPES.get(logits.dtype, -1), n, v,
+          _rows(logits, _VALUE_DTYPES, (n, v), dev, "logits"), targets.data_ptr(), logp.data_ptr(),
           None if entropy is None else entropy.data_ptr(), k, top_logp.data_ptr() if k else None,
           top_ids.data_ptr() if k else None)
-
-
-def _vector(t, dtype, n, name, dev):
-    if t.device != dev or t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} [{n}] on the logits' device")
 
 
 def widen_bf16(src: torch.Tensor, dst: torch.Tensor, stream=None):
