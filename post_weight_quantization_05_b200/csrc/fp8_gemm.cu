@@ -17,6 +17,7 @@
 // as values, or as the e4m3 codes and scales that the next product takes (a
 // tile holds 128 features of a token, exactly one of that product's blocks).
 #include <atomic>
+#include <cstdlib>
 #include <cstring>
 
 #include "fp8.cuh"
@@ -50,6 +51,21 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// One thread of a converged warp.  The warp that issues the MMAs runs its loop
+// whole and elects a thread for the tcgen05 instructions alone: their operands
+// stay in uniform registers (one thread looping by itself took 85 clocks per MMA
+// to move them there, more than the MMA).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0); }
 
 // Instruction descriptor, kind::f8f6f4: e4m3 x e4m3 -> f32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
@@ -103,6 +119,12 @@ __device__ __forceinline__ float exp_of(float x) {
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
     return fmaf(e, r * 0.693147181f, e);
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // act(g): SILU, g / (1 + e^-g); GELU in its exact form, g Phi(g), with Phi
@@ -189,7 +211,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
     uint32_t split;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
     const uint32_t rank = cluster_ctarank();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int tile = int(blockIdx.x / split);
     const int64_t row0 = int64_t(tile) * 128, tok0 = int64_t(blockIdx.y) * NT;
     // this CTA's weight and its blocks of k
@@ -239,27 +261,28 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
             }
         }
     } else if (warp > C::SUM_WARPS) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(128, NT);
-            for (int i = 0; i < groups; ++i) {
-                const int s = i % C::STAGES, count = min(C::GROUP, blocks - i * C::GROUP);
-                const uint32_t round = uint32_t(i / C::STAGES) & 1u;
-                if (!mbar_wait(&read[s], round ^ 1u, g.st, 402)) break;
-                if (!mbar_wait(&full[s], round, g.st, 403)) break;
-                tc_fence_after();
+        constexpr uint32_t idesc = idesc_e4m3(128, NT);
+        const uint64_t desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+        for (int i = 0; i < groups; ++i) {
+            const int s = i % C::STAGES, count = min(C::GROUP, blocks - i * C::GROUP);
+            const uint32_t round = uint32_t(i / C::STAGES) & 1u;
+            bool ok = mbar_wait(&read[s], round ^ 1u, g.st, 402);
+            ok = ok && mbar_wait(&full[s], round, g.st, 403);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int q = 0; q < C::GROUP; ++q) {
                     if (q >= count) continue;
-                    const uint32_t wa = smem_u32(smem + size_t(s) * C::STAGE_BYTES + q * C::BLOCK_BYTES);
-                    const uint32_t xa = wa + TILE_BYTES;
+                    const uint64_t wd = desc0 + uint32_t(s * C::STAGE_BYTES + q * C::BLOCK_BYTES) / 16;
                     const uint32_t dt = tmem_base + uint32_t(s * C::STAGE_COLS + q * NT);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)   // 32 codes (32 bytes) of the 128-byte swizzle row
-                        umma_f8(dt, sdesc_sw128(wa + kk * 32, 16, 1024), sdesc_sw128(xa + kk * 32, 16, 1024), idesc,
-                                kk > 0 ? 1u : 0u);
+                        umma_f8(dt, wd + 2 * kk, wd + TILE_BYTES / 16 + 2 * kk, idesc, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(&done[s]);               // frees the stage and completes its accumulators
             }
+            __syncwarp();
         }
     } else {
         // ---------------- sums: thread = weight row (TMEM lane), registers = tokens
@@ -390,13 +413,19 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
 // thread, so a block's scales are one number per thread (gated: two).  One CTA
 // alone would load 48 KB a block for the same MMA work, past the 128 bytes per
 // clock that shared memory gives at the tensor cores' e4m3 rate.
+//
+// Two variations fit fewer tiles to the GPU: TN = 128 (half the weight rows, four
+// accumulators), and SPLIT pairs in a cluster that share a tile's blocks of k
+// and add their sums through distributed shared memory, a slice of the columns
+// each, in rank order.
+template <int TN, int SPLIT>
 struct Wide {
-    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int STAGES = 4;                      // three to six measured the same
-    static constexpr int SLOTS = 2;
+    static constexpr int STAGE_BYTES = TILE_BYTES + TN / 2 * 128;
+    static constexpr int STAGES = TN == 256 ? 4 : 5;      // some 128 KB; three to six of 32 KB measured the same
+    static constexpr int SLOTS = 512 / TN;
     static constexpr int SUM_WARPS = 8;
     static constexpr int PARTS = SUM_WARPS / 4;           // threads that share a token's columns
-    static constexpr int CPT = 256 / PARTS;               // columns of a thread
+    static constexpr int CPT = TN / PARTS;                // columns of a thread
     static constexpr int THREADS = 32 * (SUM_WARPS + 4);  // and a warp each for loads and MMAs, two idle
     // Registers per thread after the split between the sums' two warpgroups and
     // the third; the launch checks that they fit what it was given.
@@ -409,6 +438,8 @@ struct Wide {
                                          SUM_WARPS * RING * SCALES * 32 * 4 + 2 * PARTS * 128 * 4 +
                                          (2 * STAGES + SLOTS) * 8 + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
+    static_assert(SMEM_BYTES > 117 * 1024, "a pair that holds its TMEM until its peers are done shares its SM with no other");
+    static_assert(SPLIT == 1 || TN * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
 };
 
 __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -443,7 +474,7 @@ __device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t tiles_m, uint3
     tn = in / rows;
 }
 
-// A warp's 32 output rows of RB bytes (a power of two, 64 .. 256), staged in
+// A warp's 32 output rows of RB bytes (a power of two, 16 .. 256), staged in
 // shared memory: lane r writes row r, then the lanes write whole pieces of rows
 // to global memory (straight from the registers each 16-byte store of a warp
 // would touch 32 lines).  at(): where 16-byte chunk c of row r is kept, so that
@@ -452,7 +483,7 @@ template <int RB>
 struct Stage {
     static constexpr int CHUNKS = RB / 16;
     static __device__ __forceinline__ int at(int r, int c) {
-        return r * RB + ((c ^ (CHUNKS == 4 ? (r >> 1) & 3 : r & 7)) << 4);
+        return r * RB + ((c ^ (CHUNKS >= 8 ? r & 7 : (r * CHUNKS >> 3) & (CHUNKS - 1))) << 4);
     }
     // rows x cols elements of T go to y (row pitch ld elements); vec: y and ld allow 16-byte stores.
     template <typename T>
@@ -510,27 +541,43 @@ __device__ __forceinline__ void store_rows_as(const Args& g, uint8_t* buf, int64
         store_rows<__half, COLS>(buf, static_cast<__half*>(g.y) + at, g.ldy, rows, left, vec, lane, v);
 }
 
-template <bool GATED, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
+// Arrive on the mbarrier at `bar`'s offset in both CTAs of the pair whose even
+// CTA has rank `first` once the pair MMAs issued so far by this thread finish.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t first) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(uint16_t(3u << first))
+        : "memory");
+}
+
+template <int TN, bool GATED, int ACT, int SPLIT>
+__global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
     wide_kernel(const __grid_constant__ Maps maps, const Args g) {
-    using C = Wide;
-    constexpr int TILE_N = GATED ? 128 : 256;             // output columns of a tile
+    using C = Wide<TN, SPLIT>;
+    constexpr int TILE_N = GATED ? TN / 2 : TN;           // output columns of a tile
+    constexpr int CPT = C::CPT, PARTS = C::PARTS;
+    static_assert(!GATED || TN == 256, "a gated tile is one scale block of its output wide");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* out_all = smem + size_t(C::STAGES) * C::STAGE_BYTES;
     float* ring_all = reinterpret_cast<float*>(out_all + C::SUM_WARPS * C::OUT_BYTES);
     uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + C::SUM_WARPS * C::RING * C::SCALES * 32);  // [2][PARTS][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * C::PARTS * 128);   // CTA 0: both CTAs' loads landed
+    uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * PARTS * 128);   // even CTA: both CTAs' loads landed
     uint64_t* done = full + C::STAGES;      // both CTAs: the pair's MMAs of the stage's block are complete
-    uint64_t* tempty = done + C::STAGES;    // CTA 0: accumulator read by both CTAs' warps
+    uint64_t* tempty = done + C::STAGES;    // even CTA: accumulator read by both CTAs' warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + C::SLOTS);
 
-    const uint32_t rank = cluster_ctarank();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // at most 2^16 x 2^15 tiles
-    const uint32_t cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const uint32_t rank = cluster_ctarank(), half = rank & 1u, first = rank & ~1u;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    // at most 2^16 x 2^15 tiles; with SPLIT > 1 a cluster has one
+    const uint32_t cl = blockIdx.x / (2 * SPLIT), ncl = gridDim.x / (2 * SPLIT);
     const uint32_t tiles_m = uint32_t((g.m + 255) / 256), tiles_n = uint32_t((g.n + TILE_N - 1) / TILE_N);
     const uint32_t tiles = tiles_m * tiles_n;
+    // this pair's blocks of k
+    const uint32_t share = rank >> 1;
+    const int b0 = SPLIT == 1 ? 0 : int(int64_t(g.nkb) * share / SPLIT);
+    const int blocks = SPLIT == 1 ? g.nkb : int(int64_t(g.nkb) * (share + 1) / SPLIT) - b0;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&maps.w);
@@ -548,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
         tmem_relinquish_pair();
     }
     tc_fence_before();
-    cluster_sync();          // barriers of both CTAs initialized, TMEM allocated
+    cluster_sync();          // every CTA's barriers initialized, TMEM allocated
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
@@ -558,94 +605,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
         if (warp == C::SUM_WARPS && lane == 0) {
             // ---------------- loads (both CTAs)
-            const uint32_t full0 = mapa_shared(&full[0], 0);
-            const CUtensorMap* wmap = GATED && rank == 1 ? &maps.u : &maps.w;
+            const uint32_t full0 = mapa_shared(&full[0], first);
+            const CUtensorMap* wmap = GATED && half == 1 ? &maps.u : &maps.w;
             uint32_t it = 0;
             bool ok = true;
             for (uint32_t t = cl; t < tiles && ok; t += ncl) {
                 uint32_t tm, tn;
                 grouped_tile(t, tiles_m, tiles_n, tm, tn);
-                const int xr = int(tm * 256 + rank * 128), wr = int(tn * TILE_N + (GATED ? 0 : rank * 128));
-                for (int b = 0; b < g.nkb; ++b, ++it) {
+                const int xr = int(tm * 256 + half * 128), wr = int(tn * TILE_N + (GATED ? 0 : half * (TN / 2)));
+                for (int b = 0; b < blocks; ++b, ++it) {
                     const uint32_t s = it % C::STAGES, round = it / C::STAGES;
                     if (!mbar_wait(&done[s], (round & 1u) ^ 1u, g.st, 411)) { ok = false; break; }
                     uint8_t* base = smem + size_t(s) * C::STAGE_BYTES;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
-                    tma_load_2d_pair(base, &maps.x, b * 128, xr, full0 + s * 8u);
-                    tma_load_2d_pair(base + TILE_BYTES, wmap, b * 128, wr, full0 + s * 8u);
+                    if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+                    tma_load_2d_pair(base, &maps.x, (b0 + b) * 128, xr, full0 + s * 8u);
+                    tma_load_2d_pair(base + TILE_BYTES, wmap, (b0 + b) * 128, wr, full0 + s * 8u);
                 }
             }
         }
-        if (warp == C::SUM_WARPS + 1 && lane == 0 && rank == 0) {
-            // ---------------- MMAs (CTA 0 for the pair)
-            constexpr uint32_t idesc = idesc_e4m3(256, 256);
-            uint32_t it = 0;
+        if (warp == C::SUM_WARPS + 1 && half == 0) {
+            // ---------------- MMAs (the even CTA for the pair)
+            constexpr uint32_t idesc = idesc_e4m3(256, TN);
+            const uint64_t desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+            uint32_t s = 0, round = 0, d = 0, use = 0;    // stage and accumulator, and their rounds
             bool ok = true;
             for (uint32_t t = cl; t < tiles && ok; t += ncl) {
-                for (int b = 0; b < g.nkb; ++b, ++it) {
-                    const uint32_t s = it % C::STAGES, d = it % C::SLOTS;
-                    const uint32_t use = it / C::SLOTS;
-                    if (use > 0 && !mbar_wait_cluster(&tempty[d], (use - 1) & 1u, g.st, 412)) { ok = false; break; }
-                    if (!mbar_wait(&full[s], (it / C::STAGES) & 1u, g.st, 413)) { ok = false; break; }
+                for (int b = 0; b < blocks; ++b) {
+                    ok = mbar_wait_cluster(&tempty[d], (use & 1u) ^ 1u, g.st, 412);
+                    ok = ok && mbar_wait(&full[s], round & 1u, g.st, 413);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t xa = smem_u32(smem + size_t(s) * C::STAGE_BYTES), wa = xa + TILE_BYTES;
+                    if (elect_one()) {
+                        const uint64_t xd = desc0 + s * (C::STAGE_BYTES / 16);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_f8_pair(tmem_base + d * 256, sdesc_sw128(xa + kk * 32, 16, 1024),
-                                     sdesc_sw128(wa + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-                    umma_commit_pair_both(&done[s]);   // frees the stage and completes the accumulator
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f8_pair(tmem_base + d * TN, xd + 2 * kk, xd + TILE_BYTES / 16 + 2 * kk, idesc,
+                                         kk > 0 ? 1u : 0u);
+                        umma_commit_pair(&done[s], first);   // frees the stage and completes the accumulator
+                    }
+                    __syncwarp();
+                    if (++s == C::STAGES) { s = 0; ++round; }
+                    if (++d == C::SLOTS) { d = 0; ++use; }
                 }
             }
+        }
+        if (SPLIT > 1) {     // the sums' exchange below
+            __syncwarp();
+            cluster_sync();
+            if (GATED) cluster_sync();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SUM_REGS));
-        // ---------------- sums (both CTAs): lane = token, registers = 128 columns
+        // ---------------- sums (both CTAs): lane = token, registers = columns
         const int quad = warp & 3, part = warp >> 2;
-        constexpr int CPT = C::CPT, PARTS = C::PARTS;
-        const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
+        const int r = quad * 32 + lane;       // this thread's token of the CTA's 128
+        const uint32_t tempty0 = mapa_shared(&tempty[0], first);
         uint8_t* out_buf = out_all + warp * C::OUT_BYTES;
         float* ring = ring_all + warp * (C::RING * C::SCALES * 32) + lane;
         // accumulator columns of the two halves of this thread's sums (gated: gate and up)
-        const uint32_t c0 = GATED ? (CPT / 2) * part : CPT * part, c1 = GATED ? 128 + c0 : c0 + CPT / 2;
-        uint32_t it = 0;
+        const uint32_t c0 = GATED ? (CPT / 2) * part : CPT * part, c1 = GATED ? TN / 2 + c0 : c0 + CPT / 2;
+        uint32_t stage = 0, round = 0, slot = 0;
         uint32_t parity = 0;
         bool live = true;     // a wait that ran out: go on without waiting, so that all warps meet at the barriers
         for (uint32_t t = cl; t < tiles; t += ncl, parity ^= 1u) {
             uint32_t tm, tn;
             grouped_tile(t, tiles_m, tiles_n, tm, tn);
-            const int64_t tok = int64_t(tm) * 256 + rank * 128 + quad * 32 + lane;
-            const int64_t wrow = GATED ? int64_t(tn) : min(2 * int64_t(tn) + part * 2 / PARTS, (g.n - 1) / 128);   // row of weight scale blocks
-            const float* xs = g.xs + min(tok, g.m - 1);
-            const float* ws = g.ws + wrow * g.nkb;
-            const float* us = GATED ? g.us + wrow * g.nkb : nullptr;
-            auto fetch = [&](int b) {
-                if (b < g.nkb) {
-                    float* at = ring + (b % C::RING) * (C::SCALES * 32);
-                    copy4_async(at, xs + int64_t(b) * g.lds, tok < g.m);
-                    copy4_async(at + 32, ws + b, true);
-                    if (GATED) copy4_async(at + 64, us + b, true);
+            const int64_t tok0 = int64_t(tm) * 256 + half * 128 + quad * 32, tok = tok0 + lane;
+            // row of weight scale blocks
+            const int64_t wrow = GATED || TN == 128 ? int64_t(tn) : min(2 * int64_t(tn) + part, (g.n - 1) / 128);
+            const float* xs = g.xs + int64_t(b0) * g.lds + min(tok, g.m - 1);
+            const float* ws = g.ws + wrow * g.nkb + b0;
+            const float* us = GATED ? g.us + wrow * g.nkb + b0 : nullptr;
+            const bool counted = tok < g.m;
+            int fetched = 0;
+            auto fetch = [&] {                    // the next block's scales on their way to shared memory
+                if (fetched < blocks) {
+                    float* at = ring + (fetched % C::RING) * (C::SCALES * 32);
+                    copy4_async(at, xs, counted);
+                    copy4_async(at + 32, ws + fetched, true);
+                    if (GATED) copy4_async(at + 64, us + fetched, true);
+                    xs += g.lds;
                 }
+                ++fetched;
                 asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            float s0, s1;
+            auto scale = [&](int b) {             // block b's, once at most AHEAD later ones are on their way
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
+                const float* at = ring + (b % C::RING) * (C::SCALES * 32);
+                s0 = at[0] * at[32];
+                s1 = GATED ? at[0] * at[64] : s0;
             };
             float acc[CPT];
 #pragma unroll
             for (int c = 0; c < CPT; ++c) acc[c] = 0.0f;
-            for (int b = 0; b < C::AHEAD; ++b) fetch(b);
-            for (int b = 0; b < g.nkb; ++b, ++it) {
-                const uint32_t d = it % C::SLOTS;
-                fetch(b + C::AHEAD);
-                asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
-                const float* at = ring + (b % C::RING) * (C::SCALES * 32);
-                const float s0 = at[0] * at[32], s1 = GATED ? at[0] * at[64] : s0;
-                if (live) live = mbar_wait(&done[it % C::STAGES], (it / C::STAGES) & 1u, g.st, 414);
+            for (int b = 0; b <= C::AHEAD; ++b) fetch();
+            scale(0);
+            for (int b = 0; b < blocks; ++b) {
+                if (live) live = mbar_wait(&done[stage], round & 1u, g.st, 414);
                 live = __all_sync(0xFFFFFFFFu, live);
                 tc_fence_after();
-                const uint32_t dt = tmem_base + (uint32_t(quad * 32) << 16) + d * 256;
+                const uint32_t dt = tmem_base + (uint32_t(quad * 32) << 16) + slot * TN;
                 // 16 columns at a time, the next ones on their way while these are added
                 constexpr int STEPS = CPT / 16;
                 auto column = [&](int j) { return dt + (j < STEPS / 2 ? c0 + 16 * j : c1 + 16 * (j - STEPS / 2)); };
                 uint32_t v[2][16];
                 tmem_ld_x16(column(0), v[0]);
+                const float f0 = s0, f1 = s1;
+                fetch();
 #pragma unroll
                 for (int j = 0; j < STEPS; ++j) {
                     tmem_ld_done(v[j & 1]);
@@ -654,58 +722,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                     } else {                  // this warp has read its part of the accumulator
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + d * 8u);
+                        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + slot * 8u);
+                        scale(b + 1);         // (behind the last block: values that nothing uses)
                     }
 #pragma unroll
                     for (int i = 0; i < 16; i += 2)
-                        add_scaled2(acc + 16 * j + i, v[j & 1] + i, j < STEPS / 2 ? s0 : s1);
+                        add_scaled2(acc + 16 * j + i, v[j & 1] + i, j < STEPS / 2 ? f0 : f1);
+                }
+                if (++stage == C::STAGES) { stage = 0; ++round; }
+                if (++slot == C::SLOTS) slot = 0;
+            }
+            // This thread's columns of the output: all of its sums, or of the
+            // tile's whole sums a slice (gated: of the gate's and of the up's).
+            constexpr int MINE = CPT / SPLIT, OC = GATED ? MINE / 2 : MINE;
+            float* v = acc;
+            if constexpr (SPLIT > 1) {
+                float* sums = reinterpret_cast<float*>(smem);     // [TN][128]; every load and MMA is complete
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) sums[(part * CPT + c) * 128 + r] = acc[c];
+                __syncwarp();
+                cluster_sync();
+#pragma unroll
+                for (int c = 0; c < MINE; ++c) {
+                    const int column = part * CPT + int(share) * OC + (c < OC ? c : CPT / 2 + c - OC);
+                    acc[c] = 0.0f;
+#pragma unroll
+                    for (uint32_t q = 0; q < SPLIT; ++q)
+                        acc[c] += ld_cluster_f32(mapa_shared(sums + column * 128 + r, 2 * q + half));
                 }
             }
-            if (!GATED) {
-                store_rows_as<CPT>(g, out_buf, tok - lane, int64_t(tn) * 256 + part * CPT, lane, acc);
-                continue;
-            }
-            constexpr int OC = CPT / 2;
-            const int64_t col = int64_t(tn) * 128 + part * OC;
-            uint32_t top = 0;
+            const int64_t col = int64_t(tn) * TILE_N + part * (GATED ? CPT / 2 : CPT) + (SPLIT > 1 ? int(share) * OC : 0);
+            if constexpr (!GATED) {
+                store_rows_as<OC>(g, out_buf, tok0, col, lane, v);
+            } else {
+                uint32_t top = 0;
 #pragma unroll
-            for (int c = 0; c < OC; ++c) {
-                acc[c] = gate_act<ACT>(acc[c]) * acc[OC + c];
-                top = max(top, __float_as_uint(acc[c]) & 0x7FFFFFFFu);
-            }
-            if (g.out != OUT_CODES) {
-                store_rows_as<OC>(g, out_buf, tok - lane, col, lane, acc);
-                continue;
-            }
-            // the block's maximum is over this thread's columns and the other parts'
-            const int r = quad * 32 + lane;
-            amax[(parity * PARTS + part) * 128 + r] = top;
-            named_barrier_sync(1, 32 * C::SUM_WARPS);
+                for (int c = 0; c < OC; ++c) {
+                    v[c] = gate_act<ACT>(v[c]) * v[OC + c];
+                    top = max(top, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+                }
+                // the block's maximum is over this thread's columns and those of the other parts and pairs
+                uint32_t* tops = amax + parity * PARTS * 128;
+                tops[part * 128 + r] = top;
+                if constexpr (SPLIT > 1) {
+                    __syncwarp();
+                    cluster_sync();
+                } else if (g.out == OUT_CODES) {
+                    named_barrier_sync(1, 32 * C::SUM_WARPS);
+                }
+                if (g.out != OUT_CODES) {
+                    store_rows_as<OC>(g, out_buf, tok0, col, lane, v);
+                    continue;
+                }
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) top = max(top, amax[(parity * PARTS + q) * 128 + r]);
-            float s = block_scale(top);
-            if (part == 0 && tok < g.m) {
-                g.ys[int64_t(tn) * g.ldys + tok] = s;
-                if (top >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, int(tok));
-            }
-            if (s < SMALL_SCALE) {
-                s *= SMALL_LIFT;
+                for (uint32_t q = 0; q < SPLIT; ++q)
 #pragma unroll
-                for (int c = 0; c < OC; ++c) acc[c] *= SMALL_LIFT;
-            }
-            const Coder code(s, rcp_approx(s));
+                    for (int o = 0; o < PARTS; ++o)
+                        top = max(top, SPLIT > 1 ? ld_cluster_u32(mapa_shared(tops + o * 128 + r, 2 * q + half))
+                                                 : tops[o * 128 + r]);
+                float s = block_scale(top);
+                if (part == 0 && share == 0 && tok < g.m) {
+                    g.ys[int64_t(tn) * g.ldys + tok] = s;
+                    if (top >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, int(tok));
+                }
+                if (s < SMALL_SCALE) {
+                    s *= SMALL_LIFT;
 #pragma unroll
-            for (int c = 0; c < OC; c += 16)
-                *reinterpret_cast<uint4*>(out_buf + Stage<OC>::at(lane, c / 16)) =
-                    make_uint4(code.four(acc + c), code.four(acc + c + 4), code.four(acc + c + 8), code.four(acc + c + 12));
-            Stage<OC>::flush(out_buf, static_cast<uint8_t*>(g.y) + (tok - lane) * g.ldy + col, g.ldy,
-                             int(max(int64_t(0), min(g.m - (tok - lane), int64_t(32)))),
-                             int(max(int64_t(0), min(g.n - col, int64_t(OC)))), true, lane);
+                    for (int c = 0; c < OC; ++c) v[c] *= SMALL_LIFT;
+                }
+                const Coder code(s, rcp_approx(s));
+#pragma unroll
+                for (int c = 0; c < OC; c += 16)
+                    *reinterpret_cast<uint4*>(out_buf + Stage<OC>::at(lane, c / 16)) =
+                        make_uint4(code.four(v + c), code.four(v + c + 4), code.four(v + c + 8), code.four(v + c + 12));
+                Stage<OC>::flush(out_buf, static_cast<uint8_t*>(g.y) + tok0 * g.ldy + col, g.ldy,
+                                 int(max(int64_t(0), min(g.m - tok0, int64_t(32)))),
+                                 int(max(int64_t(0), min(g.n - col, int64_t(OC)))), true, lane);
+            }
         }
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();          // no remote arrival or pair MMA is still pending
+    cluster_sync();          // no remote arrival, pair MMA or read of a peer's sums is still pending
     if (warp == C::SUM_WARPS) tmem_dealloc_pair(tmem_base, 512);
 }
 
@@ -794,14 +892,14 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
     return GPTQ_OK;
 }
 
-template <bool GATED, int ACT = 0>
+template <int TN, bool GATED, int ACT, int SPLIT>
 int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
-    auto kernel = fp8::wide_kernel<GATED, ACT>;
+    using C = fp8::Wide<TN, SPLIT>;
+    auto kernel = fp8::wide_kernel<TN, GATED, ACT, SPLIT>;
     static std::atomic<bool> ready[kMaxDev];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || sm_count(dev, &sms)) return GPTQ_ERR_CUDA;
     if (!ready[dev].load()) {
-        using C = fp8::Wide;
         cudaFuncAttributes attr;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM_BYTES)) !=
                 cudaSuccess ||
@@ -813,46 +911,61 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
     }
     fp8::Maps maps;
     std::memset(&maps, 0, sizeof(maps));
-    int rc = make_code_map(encode, &maps.w, p.w, p.n, p.d, p.ldw, 128);
-    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, 128);
+    int rc = make_code_map(encode, &maps.w, p.w, p.n, p.d, p.ldw, TN / 2);
+    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, TN / 2);
     if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, 128);
     if (rc) return rc;
-    const fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out,
-                      st};
-    const int64_t tile_n = GATED ? 128 : 256;
+    const fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, st};
+    const int64_t tile_n = GATED ? TN / 2 : TN;
     const int64_t tiles = (p.m + 255) / 256 * ((p.n + tile_n - 1) / tile_n);
-    const unsigned clusters = unsigned(std::min<int64_t>(tiles, sms / 2));
-    if (launch_pdl(kernel, dim3(2 * clusters), dim3(fp8::Wide::THREADS), fp8::Wide::SMEM_BYTES, stream, maps, g) !=
-        cudaSuccess)
-        return GPTQ_ERR_CUDA;
+    const int64_t clusters = SPLIT > 1 ? tiles : std::min<int64_t>(tiles, sms / 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(2 * SPLIT * clusters));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * SPLIT;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, maps, g) != cudaSuccess) return GPTQ_ERR_CUDA;
     count_launch();
     return GPTQ_OK;
 }
 
-// Tokens from which a product runs on SM pairs.  A build-time tuning knob.
-#ifndef GPTQ_FP8_WIDE_MIN_M
-#define GPTQ_FP8_WIDE_MIN_M 129
-#endif
-
-}  // namespace
-
 template <int ACT>
-static int launch_gated(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
-    if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<true, ACT>(p, stream, st, encode);
+int launch_gated(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
+    const char* e = getenv("WIDE"); const int w = e ? atoi(e) : 0;
+    if (w % 10 == 4) return launch_wide<256, true, ACT, 4>(p, stream, st, encode);
+    if (w % 10 == 2) return launch_wide<256, true, ACT, 2>(p, stream, st, encode);
+    if (w % 10 == 1) return launch_wide<256, true, ACT, 1>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, true, ACT>(p, stream, st, encode);
     if (p.m <= 32) return launch_narrow<32, true, ACT>(p, stream, st, encode);
-    return launch_narrow<64, true, ACT>(p, stream, st, encode);
+    if (p.m <= 64) return launch_narrow<64, true, ACT>(p, stream, st, encode);
+    return launch_wide<256, true, ACT, 1>(p, stream, st, encode);
 }
+
+}  // namespace
 
 int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
     if (p.u)
         return p.act == fp8::SILU ? launch_gated<fp8::SILU>(p, stream, st, encode)
                                   : launch_gated<fp8::GELU>(p, stream, st, encode);
-    if (p.m >= GPTQ_FP8_WIDE_MIN_M) return launch_wide<false>(p, stream, st, encode);
+    const char* e = getenv("WIDE"); const int w = e ? atoi(e) : 0;
+    if (w == 11) return launch_wide<128, false, 0, 1>(p, stream, st, encode);
+    if (w == 12) return launch_wide<128, false, 0, 2>(p, stream, st, encode);
+    if (w == 14) return launch_wide<128, false, 0, 4>(p, stream, st, encode);
+    if (w == 21) return launch_wide<256, false, 0, 1>(p, stream, st, encode);
+    if (w == 22) return launch_wide<256, false, 0, 2>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, false>(p, stream, st, encode);
     if (p.m <= 32) return launch_narrow<32, false>(p, stream, st, encode);
     if (p.m <= 64) return launch_narrow<64, false>(p, stream, st, encode);
-    return launch_narrow<128, false>(p, stream, st, encode);
+    return launch_wide<256, false, 0, 1>(p, stream, st, encode);
 }
 
 }  // namespace gptq
