@@ -17,7 +17,6 @@
 // as values, or as the e4m3 codes and scales that the next product takes (a
 // tile holds 128 features of a token, exactly one of that product's blocks).
 #include <atomic>
-#include <cstdlib>
 #include <cstring>
 
 #include "fp8.cuh"
@@ -94,6 +93,14 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
         : "r"(taddr)
         : "memory");
 }
+// N = 16 or 32 columns.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+    if constexpr (N == 16)
+        tmem_ld_x16(taddr, r);
+    else
+        tmem_ld_x32(taddr, r);
+}
 // Wait for this thread's TMEM loads; the values pass through it so that no
 // use of them can be moved in front of the wait.
 template <int N>
@@ -167,7 +174,7 @@ struct Narrow {
     // A stage is a group of blocks of k: the issuing thread's waits and its
     // commit cost about 0.34 us a stage, its MMAs 0.012 us each, against the
     // 0.37 us that one SM's share of HBM takes for a block (16 KB).
-    static constexpr int GROUP = NT <= 64 ? 2 : 1;
+    static constexpr int GROUP = 2;
     static constexpr int STAGE_BYTES = GROUP * BLOCK_BYTES;
     static constexpr int SUM_WARPS = 8;                   // two sets of four take every other stage
     static constexpr int THREADS = 32 * (SUM_WARPS + 2);  // and a warp each for loads and MMAs
@@ -178,9 +185,8 @@ struct Narrow {
     // One CTA or two per SM share its 228 KB (1 KB of them per CTA the driver's).
     // Two for up to 16 tokens leave fewer SMs idle: 11008 x 4096, 8 tokens 11.3 us
     // against 13.7 with one; for 32 they would have too few stages.
-    static constexpr int PER_SM = NT <= 32 ? 2 : 1;
-    static constexpr int FIT = (233472 / PER_SM - 1024 - 1024 - OTHER_BYTES - 256) / STAGE_BYTES;
-    static constexpr int STAGES = FIT * GROUP * NT <= 512 ? FIT : 512 / (GROUP * NT);
+    static constexpr int PER_SM = 2;
+    static constexpr int STAGES = (233472 / PER_SM - 1024 - 1024 - OTHER_BYTES - 256) / STAGE_BYTES;
     static constexpr int STAGE_COLS = GROUP * NT;  // TMEM columns: an accumulator per block of the stage
     static constexpr int COLS = STAGES * STAGE_COLS <= 64    ? 64
                                 : STAGES * STAGE_COLS <= 128 ? 128
@@ -189,7 +195,7 @@ struct Narrow {
     static constexpr int READ = 32;                      // accumulator columns read at once
     static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + OTHER_BYTES + 3 * STAGES * 8 + 16;
     // the sums that the cluster exchanges, and the gated values, reuse the stages
-    static_assert((NT <= 64 ? 3 : 2) * NT * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
+    static_assert(3 * NT * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
     static_assert(PER_SM * COLS <= 512 && STAGES * STAGE_COLS <= COLS, "TMEM columns");
     static_assert(STAGES >= 2, "a set of sum warps starts a stage's second round after the other's first");
@@ -707,27 +713,29 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                 live = __all_sync(0xFFFFFFFFu, live);
                 tc_fence_after();
                 const uint32_t dt = tmem_base + (uint32_t(quad * 32) << 16) + slot * TN;
-                // 16 columns at a time, the next ones on their way while these are added
-                constexpr int STEPS = CPT / 16;
-                auto column = [&](int j) { return dt + (j < STEPS / 2 ? c0 + 16 * j : c1 + 16 * (j - STEPS / 2)); };
-                uint32_t v[2][16];
-                tmem_ld_x16(column(0), v[0]);
+                // a chunk of columns at a time, the next one on its way while this is added
+                constexpr int CHUNK = TN == 256 ? 32 : 16, STEPS = CPT / CHUNK;
+                auto column = [&](int j) {
+                    return dt + (j < STEPS / 2 ? c0 + CHUNK * j : c1 + CHUNK * (j - STEPS / 2));
+                };
+                uint32_t v[2][CHUNK];
+                tmem_ld<CHUNK>(column(0), v[0]);
                 const float f0 = s0, f1 = s1;
-                fetch();
 #pragma unroll
                 for (int j = 0; j < STEPS; ++j) {
                     tmem_ld_done(v[j & 1]);
                     if (j + 1 < STEPS) {
-                        tmem_ld_x16(column(j + 1), v[(j + 1) & 1]);
+                        tmem_ld<CHUNK>(column(j + 1), v[(j + 1) & 1]);
                     } else {                  // this warp has read its part of the accumulator
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + slot * 8u);
+                        fetch();
                         scale(b + 1);         // (behind the last block: values that nothing uses)
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        add_scaled2(acc + 16 * j + i, v[j & 1] + i, j < STEPS / 2 ? f0 : f1);
+                    for (int i = 0; i < CHUNK; i += 2)
+                        add_scaled2(acc + CHUNK * j + i, v[j & 1] + i, j < STEPS / 2 ? f0 : f1);
                 }
                 if (++stage == C::STAGES) { stage = 0; ++round; }
                 if (++slot == C::SLOTS) slot = 0;
@@ -838,11 +846,37 @@ int sm_count(int dev, int* out) {
     return GPTQ_OK;
 }
 
+// How many clusters of `kernel` with `size` CTAs run at once.
+template <typename K>
+int resident_clusters(std::atomic<int>& cache, K kernel, int threads, size_t smem, int size, int* out) {
+    int n = cache.load();
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(size);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(unsigned(size));
+        cfg.blockDim = dim3(unsigned(threads));
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        n = std::max(1, n);
+        cache.store(n);
+    }
+    *out = n;
+    return GPTQ_OK;
+}
+
 template <int NT, bool GATED, int ACT = 0>
 int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
     using C = fp8::Narrow<NT>;
     auto kernel = fp8::narrow_kernel<NT, GATED, ACT>;
-    static std::atomic<int> resident[kMaxDev][C::MAX_SPLIT + 1];   // clusters of 1 .. MAX_SPLIT CTAs the GPU holds at once
+    static std::atomic<int> resident[kMaxDev][C::MAX_SPLIT + 1];   // clusters of 1 .. MAX_SPLIT CTAs that run at once
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return GPTQ_ERR_CUDA;
     fp8::Maps maps;
@@ -865,25 +899,17 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    if (resident[dev][1].load() == 0) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM_BYTES)) !=
-            cudaSuccess)
-            return GPTQ_ERR_CUDA;
-        for (int s = C::MAX_SPLIT; s >= 1; --s) {
-            int n = 0;
-            attr[0].val.clusterDim.x = unsigned(s);
-            cfg.gridDim = dim3(unsigned(s));
-            cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return GPTQ_ERR_CUDA;
-            resident[dev][s].store(std::max(1, n * C::PER_SM));   // (the query counts one CTA that uses TMEM per SM)
-        }
-    }
     // CTAs per tile: the most whose clusters all run at once (a cluster stays
     // inside one GPC, so that is less than the CTAs that fit).  8192 x 28672, one
     // token: 64 clusters of 4 take 38 us, of 2 47 us, of 5 (too many) 53 us.
     constexpr int STEP = GATED ? 2 : 1;      // a gated pair's CTAs come in twos
     int split = int(std::min<int64_t>(C::MAX_SPLIT, STEP * g.nkb));
-    while (split > STEP && rows * toks > resident[dev][split].load()) split -= STEP;
+    for (; split > 0; split -= STEP) {
+        int n = 0;
+        if (resident_clusters(resident[dev][split], kernel, C::THREADS, C::SMEM_BYTES, split, &n)) return GPTQ_ERR_CUDA;
+        // (the query counts one CTA that uses TMEM per SM)
+        if (split == STEP || rows * toks <= int64_t(n) * C::PER_SM) break;
+    }
     cfg.gridDim = dim3(unsigned(rows * split), unsigned(toks));
     attr[0].val.clusterDim.x = unsigned(split);
     cfg.numAttrs = 2;
@@ -938,15 +964,62 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
     return GPTQ_OK;
 }
 
+// The SM-pair form of a product: the tile width and the pairs per tile with the
+// least estimated time,
+//   rounds of tiles x (blocks of k per pair x time of a block + time of a tile),
+// a block of a 256-wide tile 430 ns and of a 128-wide one 300 (their loads and
+// their sums, not their MMAs, are what takes that long), a tile 1.5 us, 2.5 and
+// 3.5 us where 2 or 4 pairs add their sums.  Measured (us), 256-wide alone / 128
+// alone / 128 by 2 pairs / 128 by 4 / 256 by 2:
+//   256 tokens, 8192 x 28672   98 / 71 / 76 / 113 / 64
+//   256 tokens, 4096 x 4096    22 / 14 / 12.5 / 27 / 18
+//   512 tokens, 11008 x 4096   38 / 34 / 64 / 109 / 48
+//   512 tokens, 768 x 4096     18 / 11.8 / 9.5 / 8.8 / 14
+//   4096 tokens, 8192 x 4096   127 / 151 / 319 / 606 / 248
+struct WideChoice {
+    int tn, split;
+};
+int choose_wide(const Fp8Product& p, WideChoice* out) {
+    static std::atomic<int> fours[kMaxDev], eights[kMaxDev];
+    int dev = 0, sms = 0, four = 0, eight = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || sm_count(dev, &sms)) return GPTQ_ERR_CUDA;
+    using C2 = fp8::Wide<128, 2>;
+    using C4 = fp8::Wide<128, 4>;
+    if (resident_clusters(fours[dev], fp8::wide_kernel<128, false, 0, 2>, C2::THREADS, C2::SMEM_BYTES, 4, &four) ||
+        resident_clusters(eights[dev], fp8::wide_kernel<128, false, 0, 4>, C4::THREADS, C4::SMEM_BYTES, 8, &eight))
+        return GPTQ_ERR_CUDA;
+    const int64_t nkb = (p.d + 127) / 128, tiles_m = (p.m + 255) / 256;
+    const WideChoice plain[5] = {{256, 1}, {128, 1}, {256, 2}, {128, 2}, {128, 4}};
+    const WideChoice gated[3] = {{256, 1}, {256, 2}, {256, 4}};
+    const WideChoice* c = p.u ? gated : plain;
+    int64_t best = -1;
+    for (int i = 0; i < (p.u ? 3 : 5); ++i) {
+        const int64_t tile_n = p.u ? 128 : c[i].tn, tiles = tiles_m * ((p.n + tile_n - 1) / tile_n);
+        const int64_t at_once = std::max(1, c[i].split == 1 ? sms / 2 : c[i].split == 2 ? four : eight);
+        if (c[i].split > 1 && tiles > at_once) continue;      // such clusters do not follow one another
+        const int64_t rounds = (tiles + at_once - 1) / at_once, blocks = (nkb + c[i].split - 1) / c[i].split;
+        const int64_t ns = rounds * (blocks * (c[i].tn == 256 ? 430 : 300) +
+                                     (c[i].split == 1 ? 1500 : c[i].split == 2 ? 2500 : 3500));
+        if (best < 0 || ns < best) {
+            best = ns;
+            *out = c[i];
+        }
+    }
+    return GPTQ_OK;
+}
+
+// Up to this many tokens a product runs with the weights on the MMA's M side: 32
+// tokens, 8192 x 28672 41 us against 58 on SM pairs, 11008 x 4096 13.7 against 21.
+constexpr int64_t kNarrowTokens = 32;
+
 template <int ACT>
 int launch_gated(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
-    const char* e = getenv("WIDE"); const int w = e ? atoi(e) : 0;
-    if (w % 10 == 4) return launch_wide<256, true, ACT, 4>(p, stream, st, encode);
-    if (w % 10 == 2) return launch_wide<256, true, ACT, 2>(p, stream, st, encode);
-    if (w % 10 == 1) return launch_wide<256, true, ACT, 1>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, true, ACT>(p, stream, st, encode);
-    if (p.m <= 32) return launch_narrow<32, true, ACT>(p, stream, st, encode);
-    if (p.m <= 64) return launch_narrow<64, true, ACT>(p, stream, st, encode);
+    if (p.m <= kNarrowTokens) return launch_narrow<32, true, ACT>(p, stream, st, encode);
+    WideChoice c;
+    if (choose_wide(p, &c)) return GPTQ_ERR_CUDA;
+    if (c.split == 4) return launch_wide<256, true, ACT, 4>(p, stream, st, encode);
+    if (c.split == 2) return launch_wide<256, true, ACT, 2>(p, stream, st, encode);
     return launch_wide<256, true, ACT, 1>(p, stream, st, encode);
 }
 
@@ -956,15 +1029,16 @@ int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, 
     if (p.u)
         return p.act == fp8::SILU ? launch_gated<fp8::SILU>(p, stream, st, encode)
                                   : launch_gated<fp8::GELU>(p, stream, st, encode);
-    const char* e = getenv("WIDE"); const int w = e ? atoi(e) : 0;
-    if (w == 11) return launch_wide<128, false, 0, 1>(p, stream, st, encode);
-    if (w == 12) return launch_wide<128, false, 0, 2>(p, stream, st, encode);
-    if (w == 14) return launch_wide<128, false, 0, 4>(p, stream, st, encode);
-    if (w == 21) return launch_wide<256, false, 0, 1>(p, stream, st, encode);
-    if (w == 22) return launch_wide<256, false, 0, 2>(p, stream, st, encode);
     if (p.m <= 16) return launch_narrow<16, false>(p, stream, st, encode);
-    if (p.m <= 32) return launch_narrow<32, false>(p, stream, st, encode);
-    if (p.m <= 64) return launch_narrow<64, false>(p, stream, st, encode);
+    if (p.m <= kNarrowTokens) return launch_narrow<32, false>(p, stream, st, encode);
+    WideChoice c;
+    if (choose_wide(p, &c)) return GPTQ_ERR_CUDA;
+    if (c.tn == 128) {
+        if (c.split == 4) return launch_wide<128, false, 0, 4>(p, stream, st, encode);
+        if (c.split == 2) return launch_wide<128, false, 0, 2>(p, stream, st, encode);
+        return launch_wide<128, false, 0, 1>(p, stream, st, encode);
+    }
+    if (c.split == 2) return launch_wide<256, false, 0, 2>(p, stream, st, encode);
     return launch_wide<256, false, 0, 1>(p, stream, st, encode);
 }
 
