@@ -40,6 +40,59 @@ class QuantizedLinear:
     H: torch.Tensor | None = None
 
 
+@dataclasses.dataclass
+class TokenScores:
+    """Per scored position of the inputs in order: the log probability of its
+    token, the entropy of the distribution, and, if asked for, the likeliest
+    tokens."""
+    logp: torch.Tensor
+    entropy: torch.Tensor
+    scored: torch.Tensor                  # False where the target was negative
+    top_logp: torch.Tensor | None = None
+    top_ids: torch.Tensor | None = None
+
+    @property
+    def loss(self) -> float:
+        """Mean negative log probability of the scored tokens."""
+        return float(-self.logp.double().sum() / self.scored.sum())
+
+    @property
+    def perplexity(self) -> float:
+        return float(torch.exp(torch.tensor(self.loss, dtype=torch.float64)))
+
+
+@torch.no_grad()
+def token_scores(blocks, head, inputs, targets, top: int = 0, max_rows: int = 8192) -> TokenScores:
+    """What a model made of `blocks` and `head` (modules on one GPU) makes of a
+    text: the scores of `targets` (int64, one per position; negative: not scored)
+    under head(blocks(x)) for each x of `inputs`.
+
+    Source: itwiki "GPTQ", "결과" (WikiText-2 perplexity before and after
+    quantization); blog "GPTQ를 밑바닥부터 구현하며 배운 것들", section 4 (loss and
+    perplexity of the quantized model).  Call it before and after
+    BlockSequential.quantize to see what the quantization cost.  The logits exist
+    for at most `max_rows` positions at a time; `top` asks for that many of the
+    likeliest tokens (at most 32)."""
+    parts = []
+    for x, t in zip(inputs, targets, strict=True):
+        for block in blocks:
+            x = block(x)
+        x, t = x.reshape(-1, x.shape[-1]), t.reshape(-1).contiguous()
+        if x.shape[0] != t.shape[0]:
+            raise ValueError(f"{t.shape[0]} targets for {x.shape[0]} positions")
+        for xs, ts in zip(x.split(max_rows), t.split(max_rows)):
+            logits = head(xs)
+            n, dev = xs.shape[0], logits.device
+            logp, entropy = torch.empty((n,), device=dev), torch.empty((n,), device=dev)
+            top_logp = torch.empty((n, top), device=dev) if top else None
+            top_ids = torch.empty((n, top), dtype=torch.int32, device=dev) if top else None
+            api.token_logprobs(logits, ts, logp, entropy, top_logp, top_ids)
+            parts.append((logp, entropy, ts >= 0, top_logp, top_ids))
+    if not parts:
+        raise ValueError("no inputs to score")
+    return TokenScores(*(torch.cat(p) if p[0] is not None else None for p in zip(*parts)))
+
+
 class BlockSequential:
     def __init__(self, bits: int = 4, groupsize: int = -1, percdamp: float = 0.01, act_order: bool = False,
                  keep_hessian: bool = False, max_tokens: int = 32768):
