@@ -13,19 +13,24 @@
 // block joins them at the row's end.  A value costs one packed half of each of
 // a multiply-add (z, one rounding), an add and a multiply-add, and one ex2.
 // A masked value (-inf) makes 2^z z a NaN: the thread then adds that piece again,
-// and the row's others, with z bounded.  Rows that base 2 cannot hold (values past 1e9, or NaN and
-// infinities) are summed again about their maximum with every step guarded.
+// and the row's others, with z bounded.  Rows that base 2 cannot hold (values
+// past 1e9, or NaN and infinities) are summed again about their maximum with
+// every step guarded.
 //
 // The k likeliest come out of the same pass: the threads' maxima are distinct
 // elements of the row, so the k-th largest of a few of them is a threshold that
-// at least k elements reach; each thread's maximum per piece, kept in
-// shared memory, tells which values to look at again (L2 still holds them), and the few that pass are ranked by (value descending, index ascending).
-// Where too many equal the threshold, those above it and the first that equal it.
+// at least k elements reach; each thread's maximum per piece, kept in shared
+// memory, tells which values to look at again (L2 still holds them), and the few
+// that pass are ranked by (value descending, index ascending).  Where too many
+// equal the threshold, those above it and the first that equal it.  All this is
+// a row's latency, not its work, so two more warps do it, every other row each,
+// while the summing warps are in the next row.
 //
-// All this is a row's latency, not its work, so two more warps do it, every other
-// row each, while the
-// summing warps are in the next row (k = 5 over 8192 x 50257 bf16: 163 us with
-// one such warp, 157 with two; 235 when the summing threads did it).
+// Measured on a B200: 8192 x 50257 bf16 133 us without alternatives (6.2 TB/s), 157
+// with five (163 with one such warp, 235 when the summing threads did it; finer
+// maxima, per half piece, 182), 191 with twenty; 8192 x 50304 fp32 with five 241 us
+// (6.8 TB/s); one row of 128000 fp32 5.0, 8.6 and 14.6 us with none, one and
+// twenty, which is latency: the block's joins and the cluster's.
 //
 // A row is one block's, or, when there are fewer rows than the GPU has room
 // for, a cluster's: its blocks take turns in the row's pieces, and the first joins
@@ -337,15 +342,16 @@ struct Finish {
         if (nh > HITS) return -1;
         __syncwarp();
         append(in(edge), key_of(edge, e), cand, CAND, n);
-        // a lane per vector of the groups, two in flight
+        // a lane per vector of the groups, FLIGHT of them in flight (three spill)
         const uint32_t units = nh * VECS;
-        for (uint32_t u0 = 0; u0 < units; u0 += 64)
+        constexpr int FLIGHT = 2;
+        for (uint32_t u0 = 0; u0 < units; u0 += 32 * FLIGHT)
             for (uint32_t q0 = 0; q0 < per_slot; ++q0) {
-                uint32_t at[2];
-                uint4 raw[2];
-                float one[2];
+                uint32_t at[FLIGHT];
+                uint4 raw[FLIGHT];
+                float one[FLIGHT];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < FLIGHT; ++j) {
                     const uint32_t u = u0 + 32 * j + lane, hit = hits[min(u, units - 1) / VECS];
                     const uint32_t q = (hit >> 16) * per_slot + q0, p = rank + q * split;
                     const uint32_t v = (u % VECS) * THREADS + (hit & 0xFFFFu);
@@ -357,7 +363,7 @@ struct Finish {
                         raw[j] = __ldg(reinterpret_cast<const uint4*>(row.x + at[j]));
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < FLIGHT; ++j) {
                     if constexpr (E == 1) {
                         append(in(one[j]), key_of(one[j], at[j]), cand, CAND, n);
                     } else {
@@ -718,15 +724,23 @@ __global__ void __launch_bounds__(BLOCK, RESIDENT) logprobs_kernel(const Args g,
             __syncwarp();
             cluster_sync();
             if (rank == 0) {
-                float mm = LOWEST;
-                for (uint32_t q = 0; q < split; ++q) mm = fmaxf(mm, ld_cluster_f32(&total[0], q));
-                all = Sums{mm, 0.0f, 0.0f};
-                for (uint32_t q = 0; q < split; ++q) {
-                    Sums b{ld_cluster_f32(&total[0], q), ld_cluster_f32(&total[1], q), ld_cluster_f32(&total[2], q)};
-                    move_to(b, mm);
-                    all.s += b.s;
-                    all.t += b.t;
+                // a lane per block
+                Sums b{LOWEST, 0.0f, 0.0f};
+                if (lane < split) {
+                    b.m = ld_cluster_f32(&total[0], lane);
+                    b.s = ld_cluster_f32(&total[1], lane);
+                    b.t = ld_cluster_f32(&total[2], lane);
                 }
+                float mm = b.m;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(ALL, mm, o));
+                move_to(b, mm);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    b.s += __shfl_xor_sync(ALL, b.s, o);
+                    b.t += __shfl_xor_sync(ALL, b.t, o);
+                }
+                all = Sums{mm, b.s, b.t};
                 const int keys = int(split) * g.top;     // at most CAND
                 for (int c = lane; c < keys; c += 32) cand[c] = ld_cluster_u64(&best[c % g.top], uint32_t(c / g.top));
                 __syncwarp();
