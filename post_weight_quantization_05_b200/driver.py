@@ -82,6 +82,8 @@ def token_scores(blocks, head, inputs, targets, top: int = 0, max_rows: int = 81
             raise ValueError(f"{t.shape[0]} targets for {x.shape[0]} positions")
         for xs, ts in zip(x.split(max_rows), t.split(max_rows)):
             logits = head(xs)
+            if logits.stride(-1) != 1:
+                logits = logits.contiguous()
             n, dev = xs.shape[0], logits.device
             logp, entropy = torch.empty((n,), device=dev), torch.empty((n,), device=dev)
             top_logp = torch.empty((n, top), device=dev) if top else None

@@ -13,12 +13,16 @@ from torch import nn
 from . import api
 
 
+def _pitched(x: torch.Tensor) -> torch.Tensor:
+    """A matrix whose rows may be pitched, but neither strided inside nor over one another."""
+    return x if x.stride(1) == 1 and (x.shape[0] <= 1 or x.stride(0) >= x.shape[1]) else x.contiguous()
+
+
 def _rows(x: torch.Tensor) -> torch.Tensor:
-    """[..., d] as a matrix whose rows may be pitched but not strided inside."""
+    """[..., d] as such a matrix."""
     if torch.is_grad_enabled() and x.requires_grad:
         raise RuntimeError("the 8-bit layers are for inference: their inputs' gradients are not computed")
-    x = x.reshape(-1, x.shape[-1])
-    return x if x.stride(-1) == 1 else x.contiguous()
+    return _pitched(x.reshape(-1, x.shape[-1]))
 
 
 def _activations(x: torch.Tensor):
@@ -38,7 +42,7 @@ class _Fp8Module(nn.Module):
         n, d = w.shape
         codes = torch.zeros((n, -(-d // 16) * 16), dtype=torch.uint8, device=w.device)
         scales = torch.empty((api.fp8_blocks(n), api.fp8_blocks(d)), device=w.device)
-        api.fp8_quantize_weight(w if w.stride(-1) == 1 else w.contiguous(), codes[:, :d], scales)
+        api.fp8_quantize_weight(_pitched(w), codes[:, :d], scales)
         self.register_buffer(name, codes)
         self.register_buffer(name + "_scales", scales)
 
@@ -104,10 +108,20 @@ class Fp8GatedMLP(_Fp8Module):
 
 
 def quantize_linears(module: nn.Module) -> nn.Module:
-    """Replace every nn.Linear inside `module` by its 8-bit form, in place."""
-    for name, child in list(module.named_children()):
-        if isinstance(child, nn.Linear):
-            setattr(module, name, Fp8Linear(child))
-        else:
-            quantize_linears(child)
+    """Replace every nn.Linear inside `module` by its 8-bit form, in place (a
+    linear layer itself: the form is returned).  A linear that the module holds
+    in several places keeps doing so, as one form.  Subclasses of nn.Linear stay
+    as they are: others may read their weights."""
+    forms: dict[nn.Module, Fp8Linear] = {}
+
+    def form(linear):
+        if linear not in forms:
+            forms[linear] = Fp8Linear(linear)
+        return forms[linear]
+    if type(module) is nn.Linear:
+        return form(module)
+    for parent in list(module.modules()):
+        for name, child in list(parent._modules.items()):
+            if type(child) is nn.Linear:
+                setattr(parent, name, form(child))
     return module

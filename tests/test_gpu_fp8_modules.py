@@ -77,6 +77,29 @@ def test_linear_takes_any_layout_and_refuses_gradients():
         layer(x.float().requires_grad_())
 
 
+def test_linear_takes_rows_over_one_another():
+    """Broadcast and overlapping rows are inputs like any other."""
+    layer = fp8.Fp8Linear(linear(130, 256, 3))
+    x = torch.randn((1, 256), device="cuda").bfloat16()
+    assert torch.equal(layer(x.expand(9, 256)), layer(x.repeat(9, 1)))
+    windows = torch.randn((1000,), device="cuda").bfloat16().unfold(0, 256, 8)
+    assert torch.equal(layer(windows), layer(windows.contiguous()))
+
+
+def test_quantize_linears_keeps_the_structure():
+    """A linear held twice stays one, one given by itself is returned, and a
+    subclass, whose weight its owner may read, stays."""
+    class Own(nn.Linear):
+        pass
+    shared = linear(64, 64, 1)
+    m = nn.Module()
+    m.a, m.b, m.inner, m.own = shared, shared, nn.Sequential(shared, linear(64, 64, 2)), Own(64, 64)
+    assert fp8.quantize_linears(m) is m
+    assert isinstance(m.a, fp8.Fp8Linear) and m.a is m.b is m.inner[0] and m.inner[1] is not m.a
+    assert type(m.own) is Own and isinstance(m.inner[1], fp8.Fp8Linear)
+    assert isinstance(fp8.quantize_linears(linear(64, 64, 3)), fp8.Fp8Linear)
+
+
 @pytest.mark.parametrize("m", [1, 20, 300])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_gated_mlp(m, act):
@@ -136,6 +159,13 @@ def test_token_scores_of_a_stack():
     after = driver.token_scores(blocks, head, xs, targets)
     assert (after.logp - s.logp).abs().max() > 1e-3
     api.get_status()
+
+
+def test_token_scores_of_a_head_that_transposes():
+    blocks, head, xs, targets = _model(256, 4, 100, 14)
+    want = driver.token_scores(blocks, head, xs, targets)
+    got = driver.token_scores(blocks, lambda x: head(x).t().contiguous().t(), xs, targets)
+    assert torch.equal(got.logp, want.logp) and torch.equal(got.entropy, want.entropy)
 
 
 def test_token_scores_refusals():
