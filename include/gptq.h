@@ -396,7 +396,7 @@ int gptq_fp8_quantize_weight(const void* W, int dtype, int64_t d_out, int64_t d_
  *
  * with the codes' values on the right; products of codes are exact, the sum
  * inside a block and the sum over blocks are fp32, and y is rounded once to
- * its type.
+ * its type.  (xs[b][t] ws[r / 128][b] is to lie in fp32's normal range.)
  *
  * gptq_fp8_gated: the first half of a gated feed-forward layer,
  *   h[t][r] = act(g[t][r]) u[t][r],  g and u the products with Wg and Wu,
@@ -414,8 +414,10 @@ int gptq_fp8_quantize_weight(const void* W, int dtype, int64_t d_out, int64_t d_
  *   ys      GPTQ_FP8: scales of h, [ceil(d_out / 128), m], pitch ldys >= m;
  *           otherwise NULL.
  *   act     0: silu, g / (1 + e^-g).  1: gelu, g Phi(g) (the exact form).
- * Sizes and overlaps as above.  Deterministic: the same call
- * gives the same bits; no workspace.
+ * Sizes and overlaps as above.  The first call of a kind sets its kernels up:
+ * a caller that records these calls (or the quantizers, or the token scores)
+ * into a stream capture makes one such call before the capture begins.
+ * Deterministic: the same call gives the same bits; no workspace.
  * ---------------------------------------------------------------------- */
 #define GPTQ_FP8 3
 int gptq_fp8_gemm(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, const uint8_t* w, int64_t ldw,

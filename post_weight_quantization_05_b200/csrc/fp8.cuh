@@ -177,9 +177,6 @@ __device__ __forceinline__ void widen8(const Raw8<__half>& r, float* v) {
         v[2 * i + 1] = f.y;
     }
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) { widen8(load_raw8(p), v); }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) { widen8(load_raw8(p), v); }
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) { widen8(load_raw8(p), v); }
 
 // The largest magnitude of eight values in the type's own bits (16-bit types:
 // one in each half of the word, to be joined by top_of), and as fp32 bits.

@@ -5,11 +5,16 @@
 //
 // The scales change every 128 values of k, so they cannot wait for the
 // epilogue: the MMAs of one block of k (four of K = 32, one 128-byte swizzle
-// row of codes) fill a TMEM accumulator of their own, and four warps then read
+// row of codes) fill a TMEM accumulator of their own, and eight warps then read
 // it and add it, times the block's scales, to the tile's sums in fp32 registers.
 // A ring of accumulators keeps the tensor cores running meanwhile.  Sums inside
 // a block are the tensor core's fp32 accumulation; products of two e4m3
-// values are exact there.
+// values are exact there.  A block's scales are two fp32 numbers multiplied: a
+// product of scales outside fp32's normal range (2^-126 .. 2^128) loses accuracy
+// or overflows.
+//
+// Few tokens are bound by HBM (the weight's codes), prompts by the accumulators'
+// way from TMEM to the sums; either kernel below says how far it gets.
 //
 // The gated pair runs both products of the same tokens in one kernel, so the
 // tokens' codes are read once and neither product is written out:
@@ -137,11 +142,12 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // act(g): SILU, g / (1 + e^-g); GELU in its exact form, g Phi(g), with Phi
 // from erfc so that large negative gates keep their relative accuracy.  The
 // reciprocal of e^88 is below the normal numbers and counts as 0.
+// (The clamps keep exp_of's products finite.)
 constexpr int SILU = 0, GELU = 1;
 template <int ACT>
 __device__ __forceinline__ float gate_act(float g) {
     if (ACT == SILU) {
-        return g * rcp_approx(1.0f + exp_of(fminf(-g, 88.0f)));
+        return g * rcp_approx(1.0f + exp_of(fminf(fmaxf(-g, -127.0f), 88.0f)));
     }
     return 0.5f * g * erfcf(g * -0.70710678118654752f);
 }
@@ -167,13 +173,16 @@ __device__ __forceinline__ void copy4_async(float* dst, const float* src, bool l
 // The cluster's CTAs share a tile's blocks of k -- a gated pair's even ones the
 // gate's, the odd ones the up projection's -- and add their sums through
 // distributed shared memory in rank order: no workspace, no atomics, the same
-// bits on every call.
+// bits on every call.  Measured: 8192 x 28672, one token 37.6 us (6.24 TB/s);
+// a pair of 11008 x 4096 weights, 4 tokens 18.6 us (4.9 TB/s: 13.8 us of reading
+// and what start, exchange and codes take).
 template <int NT>
 struct Narrow {
     static constexpr int BLOCK_BYTES = TILE_BYTES + NT * 128;
-    // A stage is a group of blocks of k: the issuing thread's waits and its
-    // commit cost about 0.34 us a stage, its MMAs 0.012 us each, against the
-    // 0.37 us that one SM's share of HBM takes for a block (16 KB).
+    // A stage is a group of blocks of k: the waits, the commit and the sums' start
+    // cost about 0.3 us a stage, against the 0.37 us that one SM's share of HBM
+    // takes for a block (16 KB).  8192 x 28672, one token: 46 us with one block a
+    // stage, 37.6 with two.
     static constexpr int GROUP = 2;
     static constexpr int STAGE_BYTES = GROUP * BLOCK_BYTES;
     static constexpr int SUM_WARPS = 8;                   // two sets of four take every other stage
@@ -182,9 +191,8 @@ struct Narrow {
     static constexpr int AHEAD = 2, RING = 4;            // stages of scales per warp, in flight and kept
     static constexpr int ENTRY = GROUP * (NT + 4);       // floats of one: per block the tokens', then the weights'
     static constexpr int OTHER_BYTES = (SUM_WARPS * RING * ENTRY + 4 * NT) * 4;
-    // One CTA or two per SM share its 228 KB (1 KB of them per CTA the driver's).
-    // Two for up to 16 tokens leave fewer SMs idle: 11008 x 4096, 8 tokens 11.3 us
-    // against 13.7 with one; for 32 they would have too few stages.
+    // Two CTAs share an SM's 228 KB (1 KB of them per CTA the driver's): fewer SMs
+    // idle than with one.  11008 x 4096, 8 tokens: 11.3 us against 13.7.
     static constexpr int PER_SM = 2;
     static constexpr int STAGES = (233472 / PER_SM - 1024 - 1024 - OTHER_BYTES - 256) / STAGE_BYTES;
     static constexpr int STAGE_COLS = GROUP * NT;  // TMEM columns: an accumulator per block of the stage
@@ -254,6 +262,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
     const int groups = (blocks + C::GROUP - 1) / C::GROUP;
     if (warp == C::SUM_WARPS) {
         if (lane == 0) {
+            int issued = 0;
             for (int i = 0; i < groups; ++i) {
                 const int s = i % C::STAGES, count = min(C::GROUP, blocks - i * C::GROUP);
                 if (!mbar_wait(&done[s], (uint32_t(i / C::STAGES) & 1u) ^ 1u, g.st, 401)) break;
@@ -264,7 +273,11 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
                     tma_load_2d(base, wmap, k, int(row0), &full[s]);
                     tma_load_2d(base + TILE_BYTES, &maps.x, k, int(tok0), &full[s]);
                 }
+                issued = i + 1;
             }
+            // the last copies land before the CTA goes on, even where the MMAs gave up on them
+            for (int i = max(0, issued - C::STAGES); i < issued; ++i)
+                mbar_wait(&full[i % C::STAGES], uint32_t(i / C::STAGES) & 1u, g.st, 405);
         }
     } else if (warp > C::SUM_WARPS) {
         constexpr uint32_t idesc = idesc_e4m3(128, NT);
@@ -419,6 +432,12 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
 // thread, so a block's scales are one number per thread (gated: two).  One CTA
 // alone would load 48 KB a block for the same MMA work, past the 128 bytes per
 // clock that shared memory gives at the tensor cores' e4m3 rate.
+//
+// Measured: 4096 tokens, 8192 x 28672 836 us (2303 TFLOP/s; 948 before the MMAs
+// were issued by an elected thread and the scales fetched behind the accumulator's
+// release).  A block takes 830 clocks there, not 512: the sums' warps read 128 KB
+// of TMEM and make 32768 multiply-adds for it, and sixteen of them, with half the
+// columns each, were slower.  A tile's start and output add some 4700 clocks.
 //
 // Two variations fit fewer tiles to the GPU: TN = 128 (half the weight rows, four
 // accumulators), and SPLIT pairs in a cluster that share a tile's blocks of k
@@ -613,7 +632,7 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
             // ---------------- loads (both CTAs)
             const uint32_t full0 = mapa_shared(&full[0], first);
             const CUtensorMap* wmap = GATED && half == 1 ? &maps.u : &maps.w;
-            uint32_t it = 0;
+            uint32_t it = 0;     // blocks asked for so far
             bool ok = true;
             for (uint32_t t = cl; t < tiles && ok; t += ncl) {
                 uint32_t tm, tn;
@@ -628,6 +647,10 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                     tma_load_2d_pair(base + TILE_BYTES, wmap, (b0 + b) * 128, wr, full0 + s * 8u);
                 }
             }
+            // the pair's last copies land before it goes on, even where the MMAs gave up on them
+            if (half == 0)
+                for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
+                    mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1u, g.st, 415);
         }
         if (warp == C::SUM_WARPS + 1 && half == 0) {
             // ---------------- MMAs (the even CTA for the pair)

@@ -6,7 +6,10 @@
 //
 // One pass: a block's values stay in registers between its maximum and its
 // codes, so each value is read once and one byte is written for it.  The
-// bound is HBM: 3 bytes a value (bf16) or 5 (fp32).
+// bound is HBM: 3 bytes a value (bf16) or 5 (fp32).  Measured: rows 8192 x 11008
+// bf16 53 us (5.1 TB/s; 103 with a division per value, 74 with a branch for the
+// quotients next to a middle), weight 8192 x 28672 bf16 129 us (5.4 TB/s): reads
+// and writes mixed, and the coder's issue slots behind them.
 #include "fp8.cuh"
 #include "kernels.h"
 

@@ -603,6 +603,9 @@ __global__ void __launch_bounds__(BLOCK, RESIDENT) logprobs_kernel(const Args g,
                     bulk_load(ring + s * PIECE, row.x + row.head + uint64_t(p) * PIECE * E, bytes, &full[s]);
                 }
             }
+            // the last copies land before the block ends, even where the sums gave up on them
+            for (uint32_t i = it < RING ? 0 : it - RING; i < it; ++i)
+                mbar_wait(&full[i % RING], (i / RING) & 1u, g.st, 425);
         }
     } else if (warp < WARPS) {
         // ---------------- sums

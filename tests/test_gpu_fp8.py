@@ -294,6 +294,61 @@ def test_layer_runs_through():
     assert err <= 2 * 2.0 ** -4
 
 
+# Every form a product of more than 32 tokens has: one, two or four SM pairs per
+# tile, tiles of 128 and 256 weight rows, several rounds of tiles per pair.
+@pytest.mark.parametrize("m,n,d", [(40, 300, 10000), (100, 4096, 4096), (512, 4096, 1000), (100, 8192, 4000),
+                                   (300, 11008, 256), (1100, 5000, 700)])
+def test_product_forms(m, n, d):
+    ops = operands(m, n, d, m + d)
+    y = torch.empty((m, n), device="cuda")
+    api.fp8_gemm(*ops, y)
+    ref, a = reference(*ops)
+    assert (np.abs(y.double().cpu().numpy() - ref) <= sum_tol(d) * a + 2.0 ** -24 * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("out", ["fp16", "fp8"])
+@pytest.mark.parametrize("m,n,d", [(40, 1000, 5000), (40, 2900, 5000), (300, 11008, 256), (1100, 3000, 700)])
+def test_gated_forms(m, n, d, out):
+    test_gated(m, n, d, "silu", out)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("m", [1, 20, 70])
+def test_gates_near_the_largest_number(m, act):
+    """Gates past 2^127: the activation is the gate itself, or nothing."""
+    one = torch.full((128, 128), 0x38, dtype=torch.uint8, device="cuda")      # 1.0
+    x = torch.zeros((m, 128), dtype=torch.uint8, device="cuda")
+    x[:, 0] = torch.where(torch.arange(m, device="cuda") % 2 == 0, 0x38, 0xB8).byte()
+    xs = torch.ones((1, m), device="cuda")
+    y = torch.empty((m, 128), device="cuda")
+    api.fp8_gated(x, xs, one, torch.full((1, 1), 3e38, device="cuda"), one, torch.full((1, 1), 2.0 ** -100, device="cuda"),
+                  y, act=act)
+    want = float(np.float32(3e38)) * 2.0 ** -100
+    got = y.double().cpu().numpy()
+    assert (np.abs(got[::2] - want) <= 16 * 2.0 ** -24 * want).all() and (got[1::2] == 0).all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Products of every shape on two streams, interleaved: each as by itself."""
+    shapes = [(1, 2048, 4096), (24, 1024, 4096), (100, 4096, 4096), (512, 4096, 1000), (300, 2048, 256)]
+    ops = [operands(m, n, d, m) for m, n, d in shapes]
+    alone = []
+    for o, (m, n, d) in zip(ops, shapes):
+        alone.append(torch.empty((m, n), device="cuda"))
+        api.fp8_gemm(*o, alone[-1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = [[torch.full_like(y, float("nan")) for y in alone] for _ in streams]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for s, ys, order in zip(streams, both, (1, -1)):
+            for i in range(len(shapes))[::order]:
+                api.fp8_gemm(*ops[i], ys[i], stream=s)
+    torch.cuda.synchronize()
+    for ys in both:
+        assert all(torch.equal(a, b) for a, b in zip(alone, ys))
+
+
 def test_refusals():
     x, w = rand(4, 256, 1), rand(128, 256, 2)
     c, s = quantized_rows(x)
