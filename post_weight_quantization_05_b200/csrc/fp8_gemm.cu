@@ -167,6 +167,11 @@ __device__ __forceinline__ void copy4_async(float* dst, const float* src, bool l
                  : "memory");
 }
 
+// 16 bytes of which the first `live` are read, zeros behind them.
+__device__ __forceinline__ void copy16_async(float* dst, const float* src, int live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live) : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Weights on the MMA's M side: a tile is 128 weight rows (one row of scale
 // blocks) by NT tokens, which keeps the tile full for one token as for 32.
@@ -433,11 +438,19 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
 // alone would load 48 KB a block for the same MMA work, past the 128 bytes per
 // clock that shared memory gives at the tensor cores' e4m3 rate.
 //
-// Measured: 4096 tokens, 8192 x 28672 836 us (2303 TFLOP/s; 948 before the MMAs
-// were issued by an elected thread and the scales fetched behind the accumulator's
-// release).  A block takes 830 clocks there, not 512: the sums' warps read 128 KB
-// of TMEM and make 32768 multiply-adds for it, and sixteen of them, with half the
-// columns each, were slower.  A tile's start and output add some 4700 clocks.
+// Two warps bring the scales: they copy a block's ahead, multiply the tokens' by
+// the weights' into a ring in shared memory, and arrive on the same barrier as the
+// block's MMAs.  (The sums' warps did it themselves before, 270 of a block's
+// clocks: 4096 tokens, a pair of 11008 x 4096, 393 us then, 343 now.)
+//
+// Measured: 4096 tokens, 8192 x 28672 822 us (2340 TFLOP/s; 948 before the MMAs
+// were issued by an elected thread), 8192 x 4096 126 us.  A block takes some 800
+// clocks, not 512.  What is in the way is the whole circle of an accumulator --
+// MMAs, their arrival, 128 KB read from TMEM and 32768 multiply-adds, the arrival
+// back -- and power: without the sums' reads and multiply-adds the same kernel
+// takes 680 us.  Tried and slower: 128 columns per MMA and accumulator, released
+// one by one, with one issuing warp or two (1110 us: A is read twice), sixteen
+// warps for the sums.  (Stages: three to six of 32 KB measured the same.)
 //
 // Two variations fit fewer tiles to the GPU: TN = 128 (half the weight rows, four
 // accumulators), and SPLIT pairs in a cluster that share a tile's blocks of k
@@ -446,21 +459,25 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
 template <int TN, int SPLIT>
 struct Wide {
     static constexpr int STAGE_BYTES = TILE_BYTES + TN / 2 * 128;
-    static constexpr int STAGES = TN == 256 ? 4 : 5;      // some 128 KB; three to six of 32 KB measured the same
+    static constexpr int STAGES = TN == 256 ? 4 : 5;      // some 128 KB
     static constexpr int SLOTS = 512 / TN;
     static constexpr int SUM_WARPS = 8;
     static constexpr int PARTS = SUM_WARPS / 4;           // threads that share a token's columns
     static constexpr int CPT = TN / PARTS;                // columns of a thread
-    static constexpr int THREADS = 32 * (SUM_WARPS + 4);  // and a warp each for loads and MMAs, two idle
+    static constexpr int THREADS = 32 * (SUM_WARPS + 4);  // and one for loads, one for MMAs, two for scales
     // Registers per thread after the split between the sums' two warpgroups and
-    // the third; the launch checks that they fit what it was given.
-    static constexpr int SUM_REGS = 216, OTHER_REGS = 72;
-    static constexpr int AHEAD = 4;                       // blocks of scales in flight per thread
-    static constexpr int RING = 8;                        // blocks of scales per warp
-    static constexpr int SCALES = 3;                      // token, weight, second weight
+    // the third; the launch checks that they fit what it was given.  (216 and 72
+    // left the sums' loop spilling.)
+    static constexpr int SUM_REGS = 232, OTHER_REGS = 40;
+    static constexpr int AHEAD = 3;                       // blocks of scales of a warp on their way
+    static constexpr int ENTRY = 128 + 4;                 // floats of one: the tokens', two of the weights
+    // Blocks of scales kept: the scales' warp is up to STAGES blocks ahead of the
+    // MMAs, which are up to SLOTS ahead of the sums.
+    static constexpr int RING = STAGES + SLOTS;
+    static constexpr int RING_BYTES = (RING * 2 * 128 + 2 * (AHEAD + 1) * ENTRY) * 4; // per token and block: two products of its scale and a weight's
     static constexpr int OUT_BYTES = 32 * 256;            // per warp: 256 bytes of 32 output rows on their way out
-    static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * OUT_BYTES +
-                                         SUM_WARPS * RING * SCALES * 32 * 4 + 2 * PARTS * 128 * 4 +
+    static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * OUT_BYTES + RING_BYTES +
+                                         2 * PARTS * 128 * 4 +
                                          (2 * STAGES + SLOTS) * 8 + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
     static_assert(SMEM_BYTES > 117 * 1024, "a pair that holds its TMEM until its peers are done shares its SM with no other");
@@ -586,10 +603,11 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* out_all = smem + size_t(C::STAGES) * C::STAGE_BYTES;
-    float* ring_all = reinterpret_cast<float*>(out_all + C::SUM_WARPS * C::OUT_BYTES);
-    uint32_t* amax = reinterpret_cast<uint32_t*>(ring_all + C::SUM_WARPS * C::RING * C::SCALES * 32);  // [2][PARTS][128]
+    float2* ring = reinterpret_cast<float2*>(out_all + C::SUM_WARPS * C::OUT_BYTES);   // [RING][128]
+    float* fetched = reinterpret_cast<float*>(ring + C::RING * 128);                   // [2][AHEAD + 1][ENTRY]
+    uint32_t* amax = reinterpret_cast<uint32_t*>(fetched + 2 * (C::AHEAD + 1) * C::ENTRY);     // [2][PARTS][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * PARTS * 128);   // even CTA: both CTAs' loads landed
-    uint64_t* done = full + C::STAGES;      // both CTAs: the pair's MMAs of the stage's block are complete
+    uint64_t* done = full + C::STAGES;      // both CTAs: the pair's MMAs of the stage's block are complete, its scales there
     uint64_t* tempty = done + C::STAGES;    // even CTA: accumulator read by both CTAs' warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + C::SLOTS);
 
@@ -610,7 +628,7 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
         tma_prefetch_desc(&maps.x);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&done[s], 1);
+            mbar_init(&done[s], 2);
         }
         for (int s = 0; s < C::SLOTS; ++s) mbar_init(&tempty[s], 2 * C::SUM_WARPS);
         fence_mbar_init();
@@ -679,6 +697,73 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                 }
             }
         }
+        if (warp >= C::SUM_WARPS + 2) {
+            // ---------------- scales (both CTAs): every other block each, four tokens a lane
+            const uint32_t mine = uint32_t(warp - C::SUM_WARPS - 2);
+            const uint32_t total = cl < tiles ? ((tiles - cl + ncl - 1) / ncl) * uint32_t(blocks) : 0;
+            float* room = fetched + mine * (C::AHEAD + 1) * C::ENTRY;
+            const float *xs = nullptr, *ws = nullptr, *us = nullptr;   // of tile t
+            const bool vec = (reinterpret_cast<uintptr_t>(g.xs) & 15u) == 0 && g.lds % 4 == 0;   // 16-byte copies
+            int left = 0;                                              // tokens of t from this lane's on
+            uint32_t t = cl, asked = mine, to = 0;
+            int next = int(mine);                                      // the next block to fetch, in tile t or behind it
+            bool known = false;
+            auto fetch = [&] {
+                if (asked < total) {
+                    for (; next >= blocks; next -= blocks) {
+                        t += ncl;
+                        known = false;
+                    }
+                    if (!known) {
+                        uint32_t tm, tn;
+                        grouped_tile(t, tiles_m, tiles_n, tm, tn);
+                        const int64_t tok = int64_t(tm) * 256 + half * 128 + (vec ? 4 * lane : lane);
+                        const int64_t row = int64_t(tn) * (GATED || TN == 128 ? 1 : 2);   // of weight scale blocks
+                        xs = g.xs + int64_t(b0) * g.lds + tok;
+                        ws = g.ws + row * g.nkb + b0;
+                        us = GATED ? g.us + row * g.nkb + b0 : g.ws + min(row + 1, (g.n - 1) / 128) * g.nkb + b0;
+                        left = int(max(int64_t(0), min(g.m - tok, int64_t(128))));
+                        known = true;
+                    }
+                    float* e = room + to * C::ENTRY;
+                    const float* x = xs + next * g.lds;
+                    if (vec) {
+                        copy16_async(e + 4 * lane, left > 0 ? x : g.xs, min(4 * left, 16));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            copy4_async(e + 32 * i + lane, left > 32 * i ? x + 32 * i : g.xs, left > 32 * i);
+                    }
+                    if (lane < 2) copy4_async(e + 128 + lane, (lane == 0 ? ws : us) + next, true);
+                    next += 2;
+                }
+                asked += 2;
+                if (++to == C::AHEAD + 1) to = 0;
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            for (int q = 0; q < C::AHEAD; ++q) fetch();
+            uint32_t s = mine, round = 0, at = mine, from = 0;
+            for (uint32_t i = mine; i < total; i += 2) {
+                fetch();
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
+                __syncwarp();                     // all lanes' copies of the block's scales have landed
+                const float* e = room + from * C::ENTRY;
+                const float w = e[128], u = e[129];
+                bool ok = mbar_wait(&done[s], (round & 1u) ^ 1u, g.st, 417);   // (see RING)
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = e[32 * k + lane];
+                    ring[at * 128 + 32 * k + lane] = make_float2(x * w, x * u);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&done[s]);
+                if ((s += 2) >= C::STAGES) { s -= C::STAGES; ++round; }
+                if ((at += 2) >= C::RING) at -= C::RING;
+                if (++from == C::AHEAD + 1) from = 0;
+            }
+        }
         if (SPLIT > 1) {     // the sums' exchange below
             __syncwarp();
             cluster_sync();
@@ -691,46 +776,18 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
         const int r = quad * 32 + lane;       // this thread's token of the CTA's 128
         const uint32_t tempty0 = mapa_shared(&tempty[0], first);
         uint8_t* out_buf = out_all + warp * C::OUT_BYTES;
-        float* ring = ring_all + warp * (C::RING * C::SCALES * 32) + lane;
         // accumulator columns of the two halves of this thread's sums (gated: gate and up)
         const uint32_t c0 = GATED ? (CPT / 2) * part : CPT * part, c1 = GATED ? TN / 2 + c0 : c0 + CPT / 2;
-        uint32_t stage = 0, round = 0, slot = 0;
+        uint32_t stage = 0, round = 0, slot = 0, at = 0;
         uint32_t parity = 0;
         bool live = true;     // a wait that ran out: go on without waiting, so that all warps meet at the barriers
         for (uint32_t t = cl; t < tiles; t += ncl, parity ^= 1u) {
             uint32_t tm, tn;
             grouped_tile(t, tiles_m, tiles_n, tm, tn);
             const int64_t tok0 = int64_t(tm) * 256 + half * 128 + quad * 32, tok = tok0 + lane;
-            // row of weight scale blocks
-            const int64_t wrow = GATED || TN == 128 ? int64_t(tn) : min(2 * int64_t(tn) + part, (g.n - 1) / 128);
-            const float* xs = g.xs + int64_t(b0) * g.lds + min(tok, g.m - 1);
-            const float* ws = g.ws + wrow * g.nkb + b0;
-            const float* us = GATED ? g.us + wrow * g.nkb + b0 : nullptr;
-            const bool counted = tok < g.m;
-            int fetched = 0;
-            auto fetch = [&] {                    // the next block's scales on their way to shared memory
-                if (fetched < blocks) {
-                    float* at = ring + (fetched % C::RING) * (C::SCALES * 32);
-                    copy4_async(at, xs, counted);
-                    copy4_async(at + 32, ws + fetched, true);
-                    if (GATED) copy4_async(at + 64, us + fetched, true);
-                    xs += g.lds;
-                }
-                ++fetched;
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            };
-            float s0, s1;
-            auto scale = [&](int b) {             // block b's, once at most AHEAD later ones are on their way
-                asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
-                const float* at = ring + (b % C::RING) * (C::SCALES * 32);
-                s0 = at[0] * at[32];
-                s1 = GATED ? at[0] * at[64] : s0;
-            };
             float acc[CPT];
 #pragma unroll
             for (int c = 0; c < CPT; ++c) acc[c] = 0.0f;
-            for (int b = 0; b <= C::AHEAD; ++b) fetch();
-            scale(0);
             for (int b = 0; b < blocks; ++b) {
                 if (live) live = mbar_wait(&done[stage], round & 1u, g.st, 414);
                 live = __all_sync(0xFFFFFFFFu, live);
@@ -743,7 +800,8 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                 };
                 uint32_t v[2][CHUNK];
                 tmem_ld<CHUNK>(column(0), v[0]);
-                const float f0 = s0, f1 = s1;
+                const float2 f = ring[at * 128 + r];
+                const float f0 = GATED || TN == 128 || part == 0 ? f.x : f.y, f1 = GATED ? f.y : f0;
 #pragma unroll
                 for (int j = 0; j < STEPS; ++j) {
                     tmem_ld_done(v[j & 1]);
@@ -753,8 +811,6 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + slot * 8u);
-                        fetch();
-                        scale(b + 1);         // (behind the last block: values that nothing uses)
                     }
 #pragma unroll
                     for (int i = 0; i < CHUNK; i += 2)
@@ -762,6 +818,7 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                 }
                 if (++stage == C::STAGES) { stage = 0; ++round; }
                 if (++slot == C::SLOTS) slot = 0;
+                if (++at == C::RING) at = 0;
             }
             // This thread's columns of the output: all of its sums, or of the
             // tile's whole sums a slice (gated: of the gate's and of the up's).
@@ -990,17 +1047,20 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
 // The SM-pair form of a product: the tile width and the pairs per tile with the
 // least estimated time,
 //   rounds of tiles x (blocks of k per pair x time of a block + time of a tile),
-// a block of a 256-wide tile 430 ns and of a 128-wide one 300 (their loads and
-// their sums, not their MMAs, are what takes that long), a tile 1.5 us, 2.5 and
-// 3.5 us where 2 or 4 pairs add their sums.  Measured (us), 256-wide alone / 128
-// alone / 128 by 2 pairs / 128 by 4 / 256 by 2:
-//   256 tokens, 8192 x 28672   98 / 71 / 76 / 113 / 64
-//   256 tokens, 4096 x 4096    22 / 14 / 12.5 / 27 / 18
-//   512 tokens, 11008 x 4096   38 / 34 / 64 / 109 / 48
-//   512 tokens, 768 x 4096     18 / 11.8 / 9.5 / 8.8 / 14
-//   4096 tokens, 8192 x 4096   127 / 151 / 319 / 606 / 248
+// fitted to these measurements (us; 256-wide tiles by 1 pair, 128-wide by 1, 256 by
+// 2, 128 by 2, 128 by 4):
+//   256 tokens, 8192 x 28672    94.7   72.7   64.8   81.3   117
+//   256 tokens, 4096 x 4096     19.3   13.5   16.0   12.5   29.1
+//   512 tokens, 11008 x 4096    36.0   33.5   48.5   68.1   115
+//   512 tokens, 768 x 4096      18.0   12.8   14.7   10.6   9.6
+//   300 tokens, 11008 x 256     8.9    7.5    26.1   37.9   83.7
+//   4096 tokens, 8192 x 4096    123    146    263    359    645
+// and for gated pairs (256 by 1, 2 and 4):
+//   64 tokens, 11008 x 4096     34.5   47.9   89.0
+//   256 tokens, 2048 x 4096     18.4   15.5   28.5
+//   64 tokens, 1024 x 8192      30.2   21.3   18.1
 struct WideChoice {
-    int tn, split;
+    int tn, split, block_ns, tile_ns;
 };
 int choose_wide(const Fp8Product& p, WideChoice* out) {
     static std::atomic<int> fours[kMaxDev], eights[kMaxDev];
@@ -1012,8 +1072,9 @@ int choose_wide(const Fp8Product& p, WideChoice* out) {
         resident_clusters(eights[dev], fp8::wide_kernel<128, false, 0, 4>, C4::THREADS, C4::SMEM_BYTES, 8, &eight))
         return GPTQ_ERR_CUDA;
     const int64_t nkb = (p.d + 127) / 128, tiles_m = (p.m + 255) / 256;
-    const WideChoice plain[5] = {{256, 1}, {128, 1}, {256, 2}, {128, 2}, {128, 4}};
-    const WideChoice gated[3] = {{256, 1}, {256, 2}, {256, 4}};
+    const WideChoice plain[5] = {
+        {256, 1, 390, 4500}, {128, 1, 310, 800}, {256, 2, 390, 6500}, {128, 2, 310, 3500}, {128, 4, 310, 4500}};
+    const WideChoice gated[3] = {{256, 1, 390, 4500}, {256, 2, 390, 6500}, {256, 4, 390, 9000}};
     const WideChoice* c = p.u ? gated : plain;
     int64_t best = -1;
     for (int i = 0; i < (p.u ? 3 : 5); ++i) {
@@ -1021,8 +1082,7 @@ int choose_wide(const Fp8Product& p, WideChoice* out) {
         const int64_t at_once = std::max(1, c[i].split == 1 ? sms / 2 : c[i].split == 2 ? four : eight);
         if (c[i].split > 1 && tiles > at_once) continue;      // such clusters do not follow one another
         const int64_t rounds = (tiles + at_once - 1) / at_once, blocks = (nkb + c[i].split - 1) / c[i].split;
-        const int64_t ns = rounds * (blocks * (c[i].tn == 256 ? 430 : 300) +
-                                     (c[i].split == 1 ? 1500 : c[i].split == 2 ? 2500 : 3500));
+        const int64_t ns = rounds * (blocks * c[i].block_ns + c[i].tile_ns);
         if (best < 0 || ns < best) {
             best = ns;
             *out = c[i];
@@ -1032,7 +1092,7 @@ int choose_wide(const Fp8Product& p, WideChoice* out) {
 }
 
 // Up to this many tokens a product runs with the weights on the MMA's M side: 32
-// tokens, 8192 x 28672 41 us against 58 on SM pairs, 11008 x 4096 13.7 against 21.
+// tokens, 8192 x 28672 41 us against 56 on SM pairs, 11008 x 4096 13.7 against 19.
 constexpr int64_t kNarrowTokens = 32;
 
 template <int ACT>

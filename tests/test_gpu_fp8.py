@@ -297,7 +297,7 @@ def test_layer_runs_through():
 # Every form a product of more than 32 tokens has: one, two or four SM pairs per
 # tile, tiles of 128 and 256 weight rows, several rounds of tiles per pair.
 @pytest.mark.parametrize("m,n,d", [(40, 300, 10000), (100, 4096, 4096), (512, 4096, 1000), (100, 8192, 4000),
-                                   (300, 11008, 256), (1100, 5000, 700)])
+                                   (300, 11008, 256), (1100, 5000, 700), (100, 8192, 8000), (2300, 4096, 2000)])
 def test_product_forms(m, n, d):
     ops = operands(m, n, d, m + d)
     y = torch.empty((m, n), device="cuda")
