@@ -328,6 +328,22 @@ def test_gates_near_the_largest_number(m, act):
     assert (np.abs(got[::2] - want) <= 16 * 2.0 ** -24 * want).all() and (got[1::2] == 0).all()
 
 
+@pytest.mark.parametrize("m", [5, 37, 301])
+def test_scales_behind_the_last_token(m):
+    """Token scales in rows that reach past the last token, aligned and not: what
+    lies there is another caller's."""
+    n, d = 300, 700
+    xc, xs, wc, ws = operands(m, n, d, m)
+    ref, a = reference(xc, xs, wc, ws)
+    for pitch, off in ((-(-m // 4) * 4 + 4, 0), (m + 6, 1), (-(-m // 4) * 4 + 4, 4)):
+        room = torch.full((xs.shape[0], pitch + off), float("nan"), device="cuda")
+        wide = room[:, off:off + m]
+        wide.copy_(xs)
+        y = torch.empty((m, n), device="cuda")
+        api.fp8_gemm(xc, wide, wc, ws, y)
+        assert (np.abs(y.double().cpu().numpy() - ref) <= sum_tol(d) * a + 2.0 ** -24 * np.abs(ref)).all()
+
+
 def test_calls_on_two_streams_at_once():
     """Products of every shape on two streams, interleaved: each as by itself."""
     shapes = [(1, 2048, 4096), (24, 1024, 4096), (100, 4096, 4096), (512, 4096, 1000), (300, 2048, 256)]
