@@ -26,11 +26,12 @@
 // a row's latency, not its work, so two more warps do it, every other row each,
 // while the summing warps are in the next row.
 //
-// Measured on a B200: 8192 x 50257 bf16 133 us without alternatives (6.2 TB/s), 157
-// with five (163 with one such warp, 235 when the summing threads did it; finer
-// maxima, per half piece, 182), 191 with twenty; 8192 x 50304 fp32 with five 241 us
-// (6.8 TB/s); one row of 128000 fp32 5.0, 8.6 and 14.6 us with none, one and
-// twenty, which is latency: the block's joins and the cluster's.
+// Measured on a B200: 8192 x 50257 bf16 134 us without alternatives (6.2 TB/s), 149
+// with five, 174 with twenty (163 and 198 when every found value was appended by a
+// ballot of its own; 235 with five when the summing threads did it; finer maxima,
+// per half piece, 182); 8192 x 50304 fp32 with five 234 us (7.0 TB/s); one row of
+// 128000 fp32 5.1, 7.5 and 13.0 us with none, one and twenty, which is latency: the
+// block's joins and the cluster's.
 //
 // A row is one block's, or, when there are fewer rows than the GPU has room
 // for, a cluster's: its blocks take turns in the row's pieces, and the first joins
@@ -299,7 +300,7 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(const uint64_t* p, uint32_t r
 // What the summing warps leave for a row's results.
 struct Parts {
     float m[WARPS], k[WARPS], s[WARPS], t[WARPS];
-    uint32_t tops[32];                       // the largest thread maxima of each warp
+    alignas(16) uint32_t tops[32];           // the largest thread maxima of each warp
 };
 
 template <typename T, int E>
@@ -329,15 +330,34 @@ struct Finish {
         uint32_t n = 0, nh = 0;
         const uint32_t e = row.edge(lane, rank);
         const float edge = e < row.vocab ? fp8::to_f32(row.x[e]) : NAN;
-        // four threads' bounds per lane and slot
-        for (uint32_t s = 0; s < slots; ++s) {
-            T b[4];
-            if constexpr (sizeof(T) == 4)
-                *reinterpret_cast<uint4*>(b) = *reinterpret_cast<const uint4*>(bounds + s * THREADS + lane * 4);
-            else
-                *reinterpret_cast<uint2*>(b) = *reinterpret_cast<const uint2*>(bounds + s * THREADS + lane * 4);
+        // four threads' bounds per lane and slot; a scan over the lanes' hits for eight slots
+        for (uint32_t s0 = 0; s0 < slots; s0 += 8) {
+            uint32_t mask = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) append(in(fp8::to_f32(b[i])), s << 16 | uint32_t(lane * 4 + i), hits, HITS, nh);
+            for (uint32_t s = 0; s < 8; ++s) {
+                if (s0 + s >= slots) break;
+                T b[4];
+                const T* from = bounds + (s0 + s) * THREADS + lane * 4;
+                if constexpr (sizeof(T) == 4)
+                    *reinterpret_cast<uint4*>(b) = *reinterpret_cast<const uint4*>(from);
+                else
+                    *reinterpret_cast<uint2*>(b) = *reinterpret_cast<const uint2*>(from);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mask |= (in(fp8::to_f32(b[i])) ? 1u : 0u) << (4 * s + i);
+            }
+            if (!__any_sync(ALL, mask != 0)) continue;
+            const uint32_t own = __popc(mask);
+            uint32_t upto = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t before = __shfl_up_sync(ALL, upto, o);
+                if (lane >= o) upto += before;
+            }
+            for (uint32_t at = nh + upto - own; mask != 0 && at < HITS; ++at, mask &= mask - 1) {
+                const uint32_t bit = __ffs(int(mask)) - 1;
+                hits[at] = (s0 + bit / 4) << 16 | (lane * 4 + bit % 4);
+            }
+            nh += __shfl_sync(ALL, upto, 31);
         }
         if (nh > HITS) return -1;
         __syncwarp();
@@ -396,15 +416,17 @@ struct Finish {
     }
     // The candidates' `top` best in order.
     __device__ __forceinline__ void rank_candidates(int n, int top) const {
+        if (lane == 0 && (n & 1)) cand[n] = 0;      // read in pairs
+        __syncwarp();
         for (int c0 = 0; c0 < n; c0 += 64) {
             const int c = c0 + lane;
             const uint64_t a = c < n ? cand[c] : 0, b = c + 32 < n ? cand[c + 32] : 0;
             int above_a = 0, above_b = 0;
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const uint64_t key = cand[i];
-                above_a += key > a;
-                above_b += key > b;
+#pragma unroll 2
+            for (int i = 0; i < n; i += 2) {
+                const ulonglong2 key = *reinterpret_cast<const ulonglong2*>(cand + i);
+                above_a += (key.x > a) + (key.y > a);
+                above_b += (key.x > b) + (key.y > b);
             }
             if (a != 0 && above_a < top) best[above_a] = a;
             if (b != 0 && above_b < top) best[above_b] = b;
@@ -412,16 +434,19 @@ struct Finish {
     }
     // best[0 .. top) from the cluster's lists: a lane holds the head of one.
     __device__ __forceinline__ void merge_lists(int top) const {
-        uint32_t next = 0;
-        uint64_t head = lane < split ? cand[lane * top] : 0;
+        const uint64_t* list = cand + lane * top;
+        const int have = lane < split ? top : 0;
+        uint64_t head = have > 0 ? list[0] : 0, second = have > 1 ? list[1] : 0;
+        int next = 2;                                 // behind `second`
         for (int q = 0; q < top; ++q) {
             const uint32_t hi = __reduce_max_sync(ALL, uint32_t(head >> 32));
             const uint32_t lo = __reduce_max_sync(ALL, uint32_t(head >> 32) == hi ? uint32_t(head) : 0u);
             const uint64_t key = uint64_t(hi) << 32 | lo;
             if (lane == 0) best[q] = key;
-            if (head == key && lane < split) {
+            if (head == key) {
+                head = second;
+                second = next < have ? list[next] : 0;
                 ++next;
-                head = next < uint32_t(top) ? cand[lane * top + next] : 0;
             }
         }
     }
@@ -431,9 +456,10 @@ struct Finish {
         const uint32_t o = tops[lane];
         int above = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const uint32_t other = __shfl_sync(ALL, o, i);
-            above += other > o || (other == o && i < lane);
+        for (int i = 0; i < 32; i += 4) {
+            const uint4 other = *reinterpret_cast<const uint4*>(tops + i);
+            above += (other.x > o || (other.x == o && i < lane)) + (other.y > o || (other.y == o && i + 1 < lane)) +
+                     (other.z > o || (other.z == o && i + 2 < lane)) + (other.w > o || (other.w == o && i + 3 < lane));
         }
         // (0, no value at all, only in rows that have fewer values than threads)
         const uint32_t thr_order = __shfl_sync(ALL, o, __ffs(int(__ballot_sync(ALL, above == top - 1))) - 1);
@@ -556,7 +582,7 @@ __global__ void __launch_bounds__(BLOCK, RESIDENT) logprobs_kernel(const Args g,
     __shared__ alignas(8) uint64_t full[RING], empty[RING];          // pieces landed, pieces read
     __shared__ alignas(8) uint64_t ready[2], taken[2];               // rows summed, rows written out
     __shared__ Parts parts[2];
-    __shared__ uint64_t cand_of[2][CAND];
+    __shared__ alignas(16) uint64_t cand_of[2][CAND];
     __shared__ uint64_t best_of[2][MAX_TOP];
     __shared__ uint32_t hits_of[2][HITS];
     __shared__ float total[3];                                       // M, S, T of this block's share
@@ -744,8 +770,13 @@ __global__ void __launch_bounds__(BLOCK, RESIDENT) logprobs_kernel(const Args g,
                     b.t += __shfl_xor_sync(ALL, b.t, o);
                 }
                 all = Sums{mm, b.s, b.t};
-                const int keys = int(split) * g.top;     // at most CAND
-                for (int c = lane; c < keys; c += 32) cand[c] = ld_cluster_u64(&best[c % g.top], uint32_t(c / g.top));
+                uint64_t keys[MAX_SPLIT];
+#pragma unroll
+                for (uint32_t q = 0; q < MAX_SPLIT; ++q)
+                    if (q < split && lane < g.top) keys[q] = ld_cluster_u64(&best[lane], q);
+#pragma unroll
+                for (uint32_t q = 0; q < MAX_SPLIT; ++q)
+                    if (q < split && lane < g.top) cand[q * g.top + lane] = keys[q];
                 __syncwarp();
                 finish.merge_lists(g.top);
                 __syncwarp();
