@@ -469,12 +469,12 @@ struct Wide {
     // the third; the launch checks that they fit what it was given.  (216 and 72
     // left the sums' loop spilling.)
     static constexpr int SUM_REGS = 232, OTHER_REGS = 40;
-    static constexpr int AHEAD = 3;                       // blocks of scales of a warp on their way
+    static constexpr int AHEAD = 2;                       // blocks of scales of a warp on their way
     static constexpr int ENTRY = 128 + 4;                 // floats of one: the tokens', two of the weights
     // Blocks of scales kept: the scales' warp is up to STAGES blocks ahead of the
     // MMAs, which are up to SLOTS ahead of the sums.
     static constexpr int RING = STAGES + SLOTS;
-    static constexpr int RING_BYTES = (RING * 2 * 128 + 2 * (AHEAD + 1) * ENTRY) * 4; // per token and block: two products of its scale and a weight's
+    static constexpr int RING_BYTES = (RING * 2 * 128 + 2 * AHEAD * ENTRY) * 4; // per token and block: two products of its scale and a weight's
     static constexpr int OUT_BYTES = 32 * 256;            // per warp: 256 bytes of 32 output rows on their way out
     static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * OUT_BYTES + RING_BYTES +
                                          2 * PARTS * 128 * 4 +
@@ -604,8 +604,8 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* out_all = smem + size_t(C::STAGES) * C::STAGE_BYTES;
     float2* ring = reinterpret_cast<float2*>(out_all + C::SUM_WARPS * C::OUT_BYTES);   // [RING][128]
-    float* fetched = reinterpret_cast<float*>(ring + C::RING * 128);                   // [2][AHEAD + 1][ENTRY]
-    uint32_t* amax = reinterpret_cast<uint32_t*>(fetched + 2 * (C::AHEAD + 1) * C::ENTRY);     // [2][PARTS][128]
+    float* fetched = reinterpret_cast<float*>(ring + C::RING * 128);                   // [2][AHEAD][ENTRY]
+    uint32_t* amax = reinterpret_cast<uint32_t*>(fetched + 2 * C::AHEAD * C::ENTRY);     // [2][PARTS][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * PARTS * 128);   // even CTA: both CTAs' loads landed
     uint64_t* done = full + C::STAGES;      // both CTAs: the pair's MMAs of the stage's block are complete, its scales there
     uint64_t* tempty = done + C::STAGES;    // even CTA: accumulator read by both CTAs' warps
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
             // ---------------- scales (both CTAs): every other block each, four tokens a lane
             const uint32_t mine = uint32_t(warp - C::SUM_WARPS - 2);
             const uint32_t total = cl < tiles ? ((tiles - cl + ncl - 1) / ncl) * uint32_t(blocks) : 0;
-            float* room = fetched + mine * (C::AHEAD + 1) * C::ENTRY;
+            float* room = fetched + mine * C::AHEAD * C::ENTRY;
             const float *xs = nullptr, *ws = nullptr, *us = nullptr;   // of tile t
             const bool vec = (reinterpret_cast<uintptr_t>(g.xs) & 15u) == 0 && g.lds % 4 == 0;   // 16-byte copies
             int left = 0;                                              // tokens of t from this lane's on
@@ -738,14 +738,13 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                     next += 2;
                 }
                 asked += 2;
-                if (++to == C::AHEAD + 1) to = 0;
+                if (++to == C::AHEAD) to = 0;
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
             for (int q = 0; q < C::AHEAD; ++q) fetch();
             uint32_t s = mine, round = 0, at = mine, from = 0;
             for (uint32_t i = mine; i < total; i += 2) {
-                fetch();
-                asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD - 1) : "memory");
                 __syncwarp();                     // all lanes' copies of the block's scales have landed
                 const float* e = room + from * C::ENTRY;
                 const float w = e[128], u = e[129];
@@ -759,9 +758,10 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&done[s]);
+                fetch();                          // into the room that has just been read
                 if ((s += 2) >= C::STAGES) { s -= C::STAGES; ++round; }
                 if ((at += 2) >= C::RING) at -= C::RING;
-                if (++from == C::AHEAD + 1) from = 0;
+                if (++from == C::AHEAD) from = 0;
             }
         }
         if (SPLIT > 1) {     // the sums' exchange below
