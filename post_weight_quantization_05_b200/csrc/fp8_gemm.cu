@@ -356,10 +356,11 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
                     const float4 sx = *reinterpret_cast<const float4*>(at + t);
                     const float w = at[NT];
                     float* sum = acc + t;
-                    sum[0] = fmaf(__uint_as_float(v[c]) * sx.x, w, sum[0]);
-                    sum[1] = fmaf(__uint_as_float(v[c + 1]) * sx.y, w, sum[1]);
-                    sum[2] = fmaf(__uint_as_float(v[c + 2]) * sx.z, w, sum[2]);
-                    sum[3] = fmaf(__uint_as_float(v[c + 3]) * sx.w, w, sum[3]);
+                    // (the scales first: a block's sum times one of them may leave fp32's range)
+                    sum[0] = fmaf(__uint_as_float(v[c]), sx.x * w, sum[0]);
+                    sum[1] = fmaf(__uint_as_float(v[c + 1]), sx.y * w, sum[1]);
+                    sum[2] = fmaf(__uint_as_float(v[c + 2]), sx.z * w, sum[2]);
+                    sum[3] = fmaf(__uint_as_float(v[c + 3]), sx.w * w, sum[3]);
                 }
             }
         }
