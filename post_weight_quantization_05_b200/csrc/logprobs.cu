@@ -565,7 +565,8 @@ struct Finish {
         return all;
     }
     __device__ __forceinline__ void write(int64_t r, const Sums& all, int64_t target, float target_x) const {
-        const float log_s = logf(all.s);
+        // S >= 1 and the entropy >= 0, which roundings may miss by 1e-7 where one token has nearly all
+        const float log_s = max_nan(logf(all.s), 0.0f);
         const bool empty = all.s == 0.0f, bad = !(all.s <= 3.4e38f);   // every logit is -inf; one is not a number
         const float nan = __uint_as_float(0x7FC00000u);
         if (lane == 0) {
@@ -578,7 +579,7 @@ struct Finish {
                 lp = empty ? -INFINITY : (target_x - all.m) - log_s;
             }
             g.logp[r] = lp;
-            if (g.entropy) g.entropy[r] = empty ? 0.0f : log_s - all.t / all.s;
+            if (g.entropy) g.entropy[r] = empty ? 0.0f : max_nan(log_s - all.t / all.s, 0.0f);
         }
         if (lane < g.top) {
             const uint64_t key = best[lane];

@@ -53,8 +53,10 @@ def check(x, targets):
     t_tol = (3 * 2.0 ** -22 + 14 * U) * e1 + 6 * U * e2 + e1 * (eps + adds) + adds * (e1 + 24) + 4 * U * (e1 + 12)
     h = lns + e1
     assert ((ent.double() - h).abs() <= ln_tol + t_tol + 2 * U * (h + lns)).all()
+    assert (ent >= 0).all()
     want = d.gather(1, targets[:, None])[:, 0] - lns
     assert ((logp.double() - want).abs() <= ln_tol + 2 * U * (want.abs() + lns)).all()
+    assert (logp <= 0).all() and (tl <= 0).all()
     order = torch.sort(w, dim=1, descending=True, stable=True)[1][:, :3]
     assert torch.equal(ti.long(), order)
     want = d.gather(1, order) - lns[:, None]
@@ -112,3 +114,14 @@ def test_far_from_zero(n):
         x = torch.full((n, VOCAB), c, device="cuda")
         x[1::2] = -c
         check(x, torch.zeros((n,), dtype=torch.int64, device="cuda"))
+
+
+@pytest.mark.parametrize("vocab", [300, 1500, 5000, 50257])
+def test_one_token_is_certain(vocab):
+    """A row that a single token has to itself: probability one, so no more than
+    0 for its logarithm and no less than 0 for the entropy."""
+    x = torch.zeros((64, vocab), device="cuda")
+    at = torch.arange(64, device="cuda") * (vocab // 64)
+    x[torch.arange(64, device="cuda"), at] = torch.linspace(20, 60, 64, device="cuda")
+    check(x, at)
+    check(x - 31.7, at)
