@@ -85,8 +85,9 @@ def token_scores(blocks, head, inputs, targets, top: int = 0, max_rows: int = 81
             if logits.stride(-1) != 1:
                 logits = logits.contiguous()
             n, dev = xs.shape[0], logits.device
-            logp, entropy = torch.empty((n,), device=dev), torch.empty((n,), device=dev)
-            top_logp = torch.empty((n, top), device=dev) if top else None
+            f32 = {"dtype": torch.float32, "device": dev}
+            logp, entropy = torch.empty((n,), **f32), torch.empty((n,), **f32)
+            top_logp = torch.empty((n, top), **f32) if top else None
             top_ids = torch.empty((n, top), dtype=torch.int32, device=dev) if top else None
             api.token_logprobs(logits, ts, logp, entropy, top_logp, top_ids)
             parts.append((logp, entropy, ts >= 0, top_logp, top_ids))

@@ -28,7 +28,7 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
 def _activations(x: torch.Tensor):
     m, d = x.shape
     codes = api.fp8_codes(m, d, device=x.device)
-    scales = torch.empty((api.fp8_blocks(d), m), device=x.device)
+    scales = torch.empty((api.fp8_blocks(d), m), dtype=torch.float32, device=x.device)
     api.fp8_quantize_rows(x, codes, scales)
     return codes, scales
 
@@ -41,7 +41,7 @@ class _Fp8Module(nn.Module):
         w = weight.detach()
         n, d = w.shape
         codes = torch.zeros((n, -(-d // 16) * 16), dtype=torch.uint8, device=w.device)
-        scales = torch.empty((api.fp8_blocks(n), api.fp8_blocks(d)), device=w.device)
+        scales = torch.empty((api.fp8_blocks(n), api.fp8_blocks(d)), dtype=torch.float32, device=w.device)
         api.fp8_quantize_weight(_pitched(w), codes[:, :d], scales)
         self.register_buffer(name, codes)
         self.register_buffer(name + "_scales", scales)
@@ -100,7 +100,7 @@ class Fp8GatedMLP(_Fp8Module):
         y = torch.empty((m, self.out_features), dtype=x.dtype, device=x.device)
         if m:
             h = api.fp8_codes(m, self.hidden, device=x.device)
-            hs = torch.empty((api.fp8_blocks(self.hidden), m), device=x.device)
+            hs = torch.empty((api.fp8_blocks(self.hidden), m), dtype=torch.float32, device=x.device)
             api.fp8_gated(*_activations(rows), *self._weight("gate", self.in_features),
                           *self._weight("up", self.in_features), h, hs, act=self.act)
             api.fp8_gemm(h, hs, *self._weight("down", self.hidden), y)

@@ -1,0 +1,48 @@
+"""What a program around the 8-bit layers and the token scores sets: torch's
+default type."""
+import pytest
+import torch
+from torch import nn
+
+from post_weight_quantization_05_b200 import api, build_lib, driver, fp8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _ready():
+    build_lib.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    api.get_status(raise_on_error=False)
+    yield
+    code, _ = api.get_status(raise_on_error=False)
+    assert code == 0
+
+
+def linear(n, d, seed):
+    m = nn.Linear(d, n, bias=False, device="cuda", dtype=torch.bfloat16)
+    with torch.no_grad():
+        m.weight.copy_(torch.randn((n, d), generator=torch.Generator().manual_seed(seed)) * d ** -0.5)
+    return m
+
+
+@pytest.mark.parametrize("default", [torch.bfloat16, torch.float16, torch.float64])
+def test_any_default_type(default):
+    """Scales and scores are fp32 whatever torch's default type is."""
+    lin, gate, up, down = linear(130, 256, 1), linear(384, 256, 2), linear(384, 256, 3), linear(256, 384, 4)
+    x = torch.randn((2, 9, 256), generator=torch.Generator().manual_seed(5)).to("cuda", torch.bfloat16)
+    t = torch.randint(0, 130, (2, 9), generator=torch.Generator().manual_seed(6)).cuda()
+
+    def outputs():
+        layer, mlp = fp8.Fp8Linear(lin), fp8.Fp8GatedMLP(gate, up, down)
+        s = driver.token_scores([mlp], layer, [x], [t], top=2)
+        assert s.logp.dtype == s.entropy.dtype == s.top_logp.dtype == torch.float32
+        return layer(x), mlp(x), s.logp, s.entropy, s.top_logp, s.top_ids
+    want = outputs()
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        got = outputs()
+    finally:
+        torch.set_default_dtype(before)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
