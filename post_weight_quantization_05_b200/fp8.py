@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import torch
 from torch import nn
+from torch.autograd import forward_ad
 
 from . import api
 
@@ -22,6 +23,8 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
     """[..., d] as such a matrix."""
     if torch.is_grad_enabled() and x.requires_grad:
         raise RuntimeError("the 8-bit layers are for inference: their inputs' gradients are not computed")
+    if forward_ad.unpack_dual(x).tangent is not None:
+        raise RuntimeError("the 8-bit layers are for inference: no tangents are computed")
     return _pitched(x.reshape(-1, x.shape[-1]))
 
 
