@@ -57,7 +57,8 @@ class _Fp8Module(nn.Module):
         scales = {k: v for k, v in self._buffers.items() if k.endswith("_scales")}
         super()._apply(fn, recurse)
         for k, v in scales.items():
-            self._buffers[k] = v.to(self._buffers[k].device)
+            if self._buffers[k].dtype != torch.float32:
+                self._buffers[k] = v.to(self._buffers[k].device)
         return self
 
 

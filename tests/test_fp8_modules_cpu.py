@@ -1,5 +1,5 @@
 """What the 8-bit layers' modules settle on the host, without a GPU: the inputs
-they refuse."""
+they refuse, and how they move between devices and types."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwad
@@ -19,3 +19,38 @@ def test_tangents_are_refused():
             fp8._rows(dual)
     with pytest.raises(RuntimeError):
         torch.func.jvp(fp8._rows, (x,), (x,))
+
+
+def held():
+    """A module with a weight's buffers, as a layer has them."""
+    m = fp8._Fp8Module()
+    m.register_buffer("codes", torch.arange(32, dtype=torch.uint8).view(2, 16))
+    m.register_buffer("codes_scales", torch.rand(1, 1))
+    return m
+
+
+def test_scales_keep_their_type():
+    m = held()
+    codes, scales = m.codes.clone(), m.codes_scales.clone()
+    for change in (m.half, m.bfloat16, m.double, m.float, lambda: m.to("cpu", torch.bfloat16)):
+        change()
+        assert m.codes_scales.dtype == torch.float32 and torch.equal(m.codes_scales, scales)
+        assert torch.equal(m.codes, codes)
+
+
+def test_to_meta_and_back():
+    """Buffers without memory get some, and a state dict fills them."""
+    m = held()
+    state = {k: v.clone() for k, v in m.state_dict().items()}
+    m.to("meta")
+    assert m.codes_scales.is_meta and m.codes.is_meta
+    m.to_empty(device="cpu")
+    m.load_state_dict(state)
+    assert torch.equal(m.codes_scales, state["codes_scales"]) and m.codes_scales.dtype == torch.float32
+
+
+def test_shared_memory():
+    m = held()
+    scales = m.codes_scales.clone()
+    m.share_memory()
+    assert m.codes_scales.is_shared() and m.codes.is_shared() and torch.equal(m.codes_scales, scales)
