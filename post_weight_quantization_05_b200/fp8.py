@@ -111,21 +111,35 @@ class Fp8GatedMLP(_Fp8Module):
         return y.reshape(*x.shape[:-1], self.out_features)
 
 
-def quantize_linears(module: nn.Module) -> nn.Module:
+# Modules of torch that in inference hand their linears' weights to a function of
+# their own, past the linears' forward.
+_READS_WEIGHTS = (nn.TransformerEncoderLayer,)
+
+
+def quantize_linears(module: nn.Module, exclude=None) -> nn.Module:
     """Replace every nn.Linear inside `module` by its 8-bit form, in place (a
     linear layer itself: the form is returned).  A linear that the module holds
-    in several places keeps doing so, as one form.  Subclasses of nn.Linear stay
-    as they are: others may read their weights."""
+    in several places keeps doing so, as one form.
+
+    The form has no `weight`, so a linear whose weight someone else reads has to
+    stay: subclasses of nn.Linear do, and those of an nn.TransformerEncoderLayer.
+    For others exclude(name, linear) says so by returning True, asked for every
+    place that holds a linear, with the place's name as module.named_modules()
+    spells it."""
     forms: dict[nn.Module, Fp8Linear] = {}
 
-    def form(linear):
+    def form(name, linear):
+        if exclude is not None and exclude(name, linear):
+            return linear
         if linear not in forms:
             forms[linear] = Fp8Linear(linear)
         return forms[linear]
     if type(module) is nn.Linear:
-        return form(module)
-    for parent in list(module.modules()):
+        return form("", module)
+    for prefix, parent in list(module.named_modules()):
+        if isinstance(parent, _READS_WEIGHTS):
+            continue
         for name, child in list(parent._modules.items()):
             if type(child) is nn.Linear:
-                setattr(parent, name, form(child))
+                setattr(parent, name, form(f"{prefix}.{name}" if prefix else name, child))
     return module

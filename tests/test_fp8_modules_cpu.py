@@ -1,8 +1,10 @@
 """What the 8-bit layers' modules settle on the host, without a GPU: the inputs
-they refuse, and how they move between devices and types."""
+they refuse, how they move between devices and types, and which layers of a
+model they replace."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwad
+from torch import nn
 
 from post_weight_quantization_05_b200 import fp8
 
@@ -54,3 +56,45 @@ def test_shared_memory():
     scales = m.codes_scales.clone()
     m.share_memory()
     assert m.codes_scales.is_shared() and m.codes.is_shared() and torch.equal(m.codes_scales, scales)
+
+
+class Form(nn.Module):
+    """Stands for Fp8Linear, which needs a GPU."""
+
+    def __init__(self, linear):
+        super().__init__()
+        self.out_features, self.in_features = linear.weight.shape
+
+    def forward(self, x):
+        return x.new_zeros((*x.shape[:-1], self.out_features))
+
+
+@pytest.mark.parametrize("nested", [False, True])
+def test_encoder_layers_keep_their_linears(nested, monkeypatch):
+    """torch's encoder layers read their linears' weights in inference: replaced,
+    their forward would fail."""
+    monkeypatch.setattr(fp8, "Fp8Linear", Form)
+    layer = nn.TransformerEncoderLayer(32, 4, 64, batch_first=True)
+    model = nn.Sequential(nn.TransformerEncoder(layer, 2) if nested else layer, nn.Linear(32, 8)).eval()
+    x = torch.randn(2, 5, 32)
+    with torch.no_grad():
+        want = model[0](x)
+        fp8.quantize_linears(model)
+        assert isinstance(model[1], Form)
+        assert torch.equal(model[0](x), want)
+        assert model(x).shape == (2, 5, 8)
+
+
+def test_excluded_linears_stay(monkeypatch):
+    monkeypatch.setattr(fp8, "Fp8Linear", Form)
+    shared = nn.Linear(8, 8)
+    m = nn.Module()
+    m.inner = nn.ModuleDict({"a": nn.Linear(8, 8), "b": nn.Linear(8, 8)})
+    m.c, m.d = shared, shared
+    seen = []
+    fp8.quantize_linears(m, exclude=lambda name, linear: seen.append((name, linear)) or name in ("inner.a", "d"))
+    assert type(m.inner.a) is nn.Linear and isinstance(m.inner.b, Form)
+    assert isinstance(m.c, Form) and m.d is shared
+    assert sorted(name for name, _ in seen) == ["c", "d", "inner.a", "inner.b"]
+    lin = nn.Linear(4, 4)
+    assert fp8.quantize_linears(lin, exclude=lambda name, _: name == "") is lin
