@@ -72,8 +72,11 @@ def token_scores(blocks, head, inputs, targets, top: int = 0, max_rows: int = 81
     perplexity of the quantized model).  Call it before and after
     BlockSequential.quantize to see what the quantization cost.  The logits exist
     for at most `max_rows` positions at a time; `top` asks for that many of the
-    likeliest tokens (at most 32)."""
-    parts = []
+    likeliest tokens (at most 32).  A target beyond the vocabulary is refused
+    once all inputs have run (inside a stream capture, where nothing can be read
+    back, it gives NaN); a position whose logits hold a NaN or +inf has NaN
+    scores and is recorded in the status word (api.get_status)."""
+    parts, beyond = [], []
     for x, t in zip(inputs, targets, strict=True):
         for block in blocks:
             x = block(x)
@@ -89,10 +92,15 @@ def token_scores(blocks, head, inputs, targets, top: int = 0, max_rows: int = 81
             logp, entropy = torch.empty((n,), **f32), torch.empty((n,), **f32)
             top_logp = torch.empty((n, top), **f32) if top else None
             top_ids = torch.empty((n, top), dtype=torch.int32, device=dev) if top else None
-            api.token_logprobs(logits, ts, logp, entropy, top_logp, top_ids)
+            far = ts >= logits.shape[-1]
+            api.token_logprobs(logits, ts.masked_fill(far, -1), logp, entropy, top_logp, top_ids)
+            beyond.append(far.any())
+            logp.masked_fill_(far, float("nan"))
             parts.append((logp, entropy, ts >= 0, top_logp, top_ids))
     if not parts:
         raise ValueError("no inputs to score")
+    if not torch.cuda.is_current_stream_capturing() and bool(torch.stack(beyond).any()):
+        raise ValueError("a target lies beyond the vocabulary")
     return TokenScores(*(torch.cat(p) if p[0] is not None else None for p in zip(*parts)))
 
 

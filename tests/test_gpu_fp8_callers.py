@@ -1,5 +1,5 @@
-"""What a program around the 8-bit layers and the token scores sets: torch's
-default type."""
+"""What a program around the 8-bit layers and the token scores sets or leaves
+behind: torch's default type, targets that are no tokens."""
 import pytest
 import torch
 from torch import nn
@@ -46,3 +46,38 @@ def test_any_default_type(default):
     finally:
         torch.set_default_dtype(before)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_targets_that_are_no_tokens():
+    """A target beyond the vocabulary is the call's error, not the next one's:
+    nothing is left in the status word."""
+    head = linear(100, 64, 7)
+    x = torch.randn((3, 8, 64), generator=torch.Generator().manual_seed(8)).to("cuda", torch.bfloat16)
+    t = torch.randint(0, 100, (3, 8), generator=torch.Generator().manual_seed(9)).cuda()
+    want = driver.token_scores([], head, [x], [t])
+    for bad in (100, 1 << 40):
+        wrong = t.clone()
+        wrong[2, 5] = bad
+        for rows in (4, 8192):
+            with pytest.raises(ValueError):
+                driver.token_scores([], head, [x, x], [t, wrong], max_rows=rows)
+    assert api.get_status(raise_on_error=False)[0] == 0
+    assert torch.equal(driver.token_scores([], head, [x], [t]).logp, want.logp)
+
+
+def test_scores_in_a_graph():
+    """Captured and replayed on other targets."""
+    head = linear(100, 64, 7)
+    x = torch.randn((8, 64), generator=torch.Generator().manual_seed(8)).to("cuda", torch.bfloat16)
+    t = torch.arange(8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        driver.token_scores([], head, [x], [t])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = driver.token_scores([], head, [x], [t])
+    t.add_(50)
+    graph.replay()
+    assert torch.equal(s.logp, driver.token_scores([], head, [x], [t]).logp)
