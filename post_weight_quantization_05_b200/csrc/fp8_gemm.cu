@@ -472,19 +472,40 @@ struct Wide {
     static constexpr int SUM_REGS = 232, OTHER_REGS = 40;
     static constexpr int AHEAD = 2;                       // blocks of scales of a warp on their way
     static constexpr int ENTRY = 128 + 4;                 // floats of one: the tokens', two of the weights
-    // Blocks of scales kept: the scales' warp is up to STAGES blocks ahead of the
-    // MMAs, which are up to SLOTS ahead of the sums.
-    static constexpr int RING = STAGES + SLOTS;
+    // Blocks of scales kept: four rounds of the stages, each with a barrier on which the
+    // sums say once that they have read it.  The scales' warps are at most STAGES
+    // blocks ahead of the MMAs, which are at most SLOTS ahead of the sums, so they never
+    // wait for room.  (The barriers cost 1% of the long products.  The same arrival
+    // behind a branch cost 4%, a wait behind one in the scales' warps 5% of 509 tokens,
+    // 11008 x 4096.)
+    static constexpr int RING = 4 * STAGES;
+    static_assert(SLOTS <= STAGES, "room for the scales ahead");
     static constexpr int RING_BYTES = (RING * 2 * 128 + 2 * AHEAD * ENTRY) * 4; // per token and block: two products of its scale and a weight's
     static constexpr int OUT_BYTES = 32 * 256;            // per warp: 256 bytes of 32 output rows on their way out
     static constexpr size_t SMEM_BYTES = 1024 + size_t(STAGES) * STAGE_BYTES + SUM_WARPS * OUT_BYTES + RING_BYTES +
                                          2 * PARTS * 128 * 4 +
-                                         (2 * STAGES + SLOTS) * 8 + 16;
+                                         (2 * STAGES + SLOTS + 4) * 8 + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
     static_assert(SMEM_BYTES > 117 * 1024, "a pair that holds its TMEM until its peers are done shares its SM with no other");
     static_assert(SPLIT == 1 || TN * 128 * 4 <= STAGES * STAGE_BYTES, "exchange buffer");
 };
 
+// Arrive on a barrier of this CTA where `yes` (predicated, without a branch).
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool yes) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(uint32_t(yes))
+        : "memory");
+}
+// Wait for two barriers, with one branch where both phases are complete.
+__device__ __forceinline__ bool mbar_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, DevStatus* st,
+                                           int where) {
+    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+    if (x && y) return true;
+    return mbar_wait(a, pa, st, where) && mbar_wait(b, pb, st, where + 1);
+}
 __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                              uint32_t accumulate) {
     asm volatile(
@@ -500,9 +521,10 @@ __device__ __forceinline__ void add_scaled2(float* a, const uint32_t* v, float s
 }
 // Arrive on an mbarrier of either CTA without publishing memory: for an
 // accumulator that has been read (its loads have returned) nothing else needs
-// to be ordered, and a release at cluster scope would wait for every copy and
-// store this thread has in flight (measured: it was the kernel's whole time,
-// 1.9 ms instead of 0.7 at 4096 x 8192 x 28672).
+// to be ordered (the scales' ring has barriers of its own), and a release at
+// cluster scope would wait for every copy and store this thread has in flight
+// (measured: it was the kernel's whole time, 1.9 ms instead of 0.7 at 4096 x 8192
+// x 28672).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -610,7 +632,8 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(amax + 2 * PARTS * 128);   // even CTA: both CTAs' loads landed
     uint64_t* done = full + C::STAGES;      // both CTAs: the pair's MMAs of the stage's block are complete, its scales there
     uint64_t* tempty = done + C::STAGES;    // even CTA: accumulator read by both CTAs' warps
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + C::SLOTS);
+    uint64_t* taken = tempty + C::SLOTS;    // [4] a round's scales read by this CTA's sums
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(taken + 4);
 
     const uint32_t rank = cluster_ctarank(), half = rank & 1u, first = rank & ~1u;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -632,6 +655,7 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
             mbar_init(&done[s], 2);
         }
         for (int s = 0; s < C::SLOTS; ++s) mbar_init(&tempty[s], 2 * C::SUM_WARPS);
+        for (int s = 0; s < 4; ++s) mbar_init(&taken[s], C::SUM_WARPS);
         fence_mbar_init();
     }
     if (warp == C::SUM_WARPS) {
@@ -743,25 +767,25 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
             for (int q = 0; q < C::AHEAD; ++q) fetch();
-            uint32_t s = mine, round = 0, at = mine, from = 0;
+            uint32_t s = mine, round = 0, from = 0;
             for (uint32_t i = mine; i < total; i += 2) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD - 1) : "memory");
                 __syncwarp();                     // all lanes' copies of the block's scales have landed
                 const float* e = room + from * C::ENTRY;
                 const float w = e[128], u = e[129];
-                bool ok = mbar_wait(&done[s], (round & 1u) ^ 1u, g.st, 417);   // (see RING)
+                bool ok = mbar_wait2(&done[s], (round & 1u) ^ 1u, &taken[round & 3u], ((round >> 2) & 1u) ^ 1u, g.st,
+                                     417);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float x = e[32 * k + lane];
-                    ring[at * 128 + 32 * k + lane] = make_float2(x * w, x * u);
+                    ring[(s + (round & 3u) * C::STAGES) * 128 + 32 * k + lane] = make_float2(x * w, x * u);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&done[s]);
                 fetch();                          // into the room that has just been read
                 if ((s += 2) >= C::STAGES) { s -= C::STAGES; ++round; }
-                if ((at += 2) >= C::RING) at -= C::RING;
                 if (++from == C::AHEAD) from = 0;
             }
         }
@@ -779,7 +803,7 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
         uint8_t* out_buf = out_all + warp * C::OUT_BYTES;
         // accumulator columns of the two halves of this thread's sums (gated: gate and up)
         const uint32_t c0 = GATED ? (CPT / 2) * part : CPT * part, c1 = GATED ? TN / 2 + c0 : c0 + CPT / 2;
-        uint32_t stage = 0, round = 0, slot = 0, at = 0;
+        uint32_t stage = 0, round = 0, slot = 0;
         uint32_t parity = 0;
         bool live = true;     // a wait that ran out: go on without waiting, so that all warps meet at the barriers
         for (uint32_t t = cl; t < tiles; t += ncl, parity ^= 1u) {
@@ -801,7 +825,7 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                 };
                 uint32_t v[2][CHUNK];
                 tmem_ld<CHUNK>(column(0), v[0]);
-                const float2 f = ring[at * 128 + r];
+                const float2 f = ring[(stage + (round & 3u) * C::STAGES) * 128 + r];
                 const float f0 = GATED || TN == 128 || part == 0 ? f.x : f.y, f1 = GATED ? f.y : f0;
 #pragma unroll
                 for (int j = 0; j < STEPS; ++j) {
@@ -817,9 +841,10 @@ __global__ void __launch_bounds__(Wide<TN, SPLIT>::THREADS, 1)
                     for (int i = 0; i < CHUNK; i += 2)
                         add_scaled2(acc + CHUNK * j + i, v[j & 1] + i, j < STEPS / 2 ? f0 : f1);
                 }
-                if (++stage == C::STAGES) { stage = 0; ++round; }
+                ++stage;
+                mbar_arrive_if(&taken[round & 3u], lane == 0 && stage == C::STAGES);
+                if (stage == C::STAGES) { stage = 0; ++round; }
                 if (++slot == C::SLOTS) slot = 0;
-                if (++at == C::RING) at = 0;
             }
             // This thread's columns of the output: all of its sums, or of the
             // tile's whole sums a slice (gated: of the gate's and of the up's).
