@@ -96,14 +96,14 @@ int fp8_product(const Fp8Product& p, void* stream) {
     if (!valid_codes(p.x, p.d, p.ldx) || !valid_f32(p.xs) || !valid_ld(p.lds, p.m) ||
         !valid_codes(p.w, p.d, p.ldw) || !valid_f32(p.ws))
         return GPTQ_ERR_INVALID_ARG;
-    if (p.u && (!valid_codes(p.u, p.d, p.ldu) || !valid_f32(p.us))) return GPTQ_ERR_INVALID_ARG;
+    if (p.u && (!valid_codes(p.u, p.d, p.ldw) || !valid_f32(p.us))) return GPTQ_ERR_INVALID_ARG;
     if (p.out == GPTQ_FP8 ? (!valid_codes(p.y, p.n, p.ldy) || !valid_f32(p.ys) || !valid_ld(p.ldys, p.m))
                           : (!valid_values(p.y, p.out) || !valid_ld(p.ldy, p.n) || p.ys))
         return GPTQ_ERR_INVALID_ARG;
     const int64_t nb = fp8_blocks(p.d);
     const Span in[6] = {pitched(p.x, p.m, p.d, p.ldx, 1),  pitched(p.xs, nb, p.m, p.lds, 4),
                         pitched(p.w, p.n, p.d, p.ldw, 1),  pitched(p.ws, fp8_blocks(p.n), nb, nb, 4),
-                        pitched(p.u, p.u ? p.n : 0, p.d, p.ldu, 1),
+                        pitched(p.u, p.u ? p.n : 0, p.d, p.ldw, 1),
                         pitched(p.us, p.u ? fp8_blocks(p.n) : 0, nb, nb, 4)};
     const Span y = pitched(p.y, p.m, p.n, p.ldy, value_bytes(p.out));
     const Span ys = pitched(p.ys, p.ys ? fp8_blocks(p.n) : 0, p.m, p.ldys, 4);
@@ -369,7 +369,7 @@ int gptq_fp8_gemm(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, c
                   const float* ws, int64_t m, int64_t d_out, int64_t d_in, int out, void* y, int64_t ldy,
                   void* stream) {
     if (!valid_value_dtype(out)) return GPTQ_ERR_INVALID_ARG;
-    const Fp8Product p{x, xs, w, ws, nullptr, nullptr, y, nullptr, m, d_out, d_in, ldx, lds, ldw, ldw, ldy, 0, out, 0};
+    const Fp8Product p{x, xs, w, ws, nullptr, nullptr, y, nullptr, m, d_out, d_in, ldx, lds, ldw, ldy, 0, out, 0};
     return fp8_product(p, stream);
 }
 
@@ -379,7 +379,7 @@ int gptq_fp8_gated(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, 
     if (!valid_value_dtype(out) && out != GPTQ_FP8) return GPTQ_ERR_INVALID_ARG;
     if (act != 0 && act != 1) return GPTQ_ERR_INVALID_ARG;
     if (m != 0 && (!Wu || !us)) return GPTQ_ERR_INVALID_ARG;   // a null second weight is the plain product below
-    const Fp8Product p{x, xs, Wg, gs, Wu, us, y, ys, m, d_out, d_in, ldx, lds, ldw, ldw, ldy, ldys, out, act};
+    const Fp8Product p{x, xs, Wg, gs, Wu, us, y, ys, m, d_out, d_in, ldx, lds, ldw, ldy, ldys, out, act};
     return fp8_product(p, stream);
 }
 

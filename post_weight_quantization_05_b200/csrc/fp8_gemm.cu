@@ -174,7 +174,8 @@ __device__ __forceinline__ void copy16_async(float* dst, const float* src, int l
 
 // ---------------------------------------------------------------------------
 // Weights on the MMA's M side: a tile is 128 weight rows (one row of scale
-// blocks) by NT tokens, which keeps the tile full for one token as for 32.
+// blocks) by all the tokens, NT at most, which keeps the tile full for one token
+// as for 32.
 // The cluster's CTAs share a tile's blocks of k -- a gated pair's even ones the
 // gate's, the odd ones the up projection's -- and add their sums through
 // distributed shared memory in rank order: no workspace, no atomics, the same
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
     const uint32_t rank = cluster_ctarank();
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int tile = int(blockIdx.x / split);
-    const int64_t row0 = int64_t(tile) * 128, tok0 = int64_t(blockIdx.y) * NT;
+    const int64_t row0 = int64_t(tile) * 128;
     // this CTA's weight and its blocks of k
     const bool up = GATED && (rank & 1u);
     const uint32_t share = GATED ? rank >> 1 : rank, shares = GATED ? split >> 1 : split;
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
                     uint8_t* base = smem + size_t(s) * C::STAGE_BYTES + q * C::BLOCK_BYTES;
                     const int k = (b0 + i * C::GROUP + q) * 128;
                     tma_load_2d(base, wmap, k, int(row0), &full[s]);
-                    tma_load_2d(base + TILE_BYTES, &maps.x, k, int(tok0), &full[s]);
+                    tma_load_2d(base + TILE_BYTES, &maps.x, k, 0, &full[s]);
                 }
                 issued = i + 1;
             }
@@ -312,14 +313,14 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
         // ---------------- sums: thread = weight row (TMEM lane), registers = tokens
         const int set = warp >> 2;
         float* ring = ring_all + warp * C::RING * C::ENTRY;
-        const float* xs = g.xs + int64_t(b0) * g.lds + tok0;
+        const float* xs = g.xs + int64_t(b0) * g.lds;
         const float* ws = (up ? g.us : g.ws) + int64_t(tile) * g.nkb + b0;
         auto fetch = [&](int i) {
             float* at = ring + ((i >> 1) % C::RING) * C::ENTRY;
 #pragma unroll
             for (int c = lane; c < C::GROUP * NT; c += 32) {
                 const int q = c / NT, t = c % NT, b = i * C::GROUP + q;
-                const bool live = b < blocks && tok0 + t < g.m;
+                const bool live = b < blocks && t < g.m;
                 copy4_async(at + q * (NT + 4) + t, live ? xs + int64_t(b) * g.lds + t : xs, live);
             }
             if (lane < C::GROUP) copy4_async(at + lane * (NT + 4) + NT, ws + min(i * C::GROUP + lane, blocks - 1), true);
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
     }
     __syncwarp();
     cluster_sync();
-    const int cols = int(min(int64_t(NT), g.m - tok0));
+    const int cols = int(g.m);
     if (warp < C::SUM_WARPS) {
         // tokens (columns) rank, rank + split, ..., every other one to each set
         const int first = int(rank) + set * int(split), step = 2 * int(split);
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
                 const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
                 if (lane == 0) amax[c * 4 + (warp & 3)] = top;
             } else if (row < g.n) {
-                store_out(g.y, (tok0 + c) * g.ldy + row, v, g.out);
+                store_out(g.y, c * g.ldy + row, v, g.out);
             }
         }
         if (GATED && g.out == OUT_CODES) {
@@ -411,15 +412,15 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
                 const uint32_t a = max(max(amax[4 * c], amax[4 * c + 1]), max(amax[4 * c + 2], amax[4 * c + 3]));
                 float s = block_scale(a), v = held[c * 128 + r];
                 if (r == 0) {
-                    g.ys[int64_t(tile) * g.ldys + tok0 + c] = s;
-                    if (a >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, int(tok0 + c));
+                    g.ys[int64_t(tile) * g.ldys + c] = s;
+                    if (a >= INF_BITS) record_error(g.st, GPTQ_ERR_NONFINITE, c);
                 }
                 if (s < SMALL_SCALE) {
                     s *= SMALL_LIFT;
                     v *= SMALL_LIFT;
                 }
                 if (row < g.n)
-                    static_cast<uint8_t*>(g.y)[(tok0 + c) * g.ldy + row] = uint8_t(Coder(s, rcp_approx(s)).one(v));
+                    static_cast<uint8_t*>(g.y)[c * g.ldy + row] = uint8_t(Coder(s, rcp_approx(s)).one(v));
             }
         }
     }
@@ -978,6 +979,7 @@ int resident_clusters(std::atomic<int>& cache, K kernel, int threads, size_t sme
     return GPTQ_OK;
 }
 
+// p.m is at most NT.
 template <int NT, bool GATED, int ACT = 0>
 int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode) {
     using C = fp8::Narrow<NT>;
@@ -988,11 +990,11 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
     fp8::Maps maps;
     std::memset(&maps, 0, sizeof(maps));
     int rc = make_code_map(encode, &maps.w, p.w, p.n, p.d, p.ldw, 128);
-    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, 128);
+    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldw, 128);
     if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, NT);
     if (rc) return rc;
     const fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, st};
-    const int64_t rows = (p.n + 127) / 128, toks = (p.m + NT - 1) / NT;
+    const int64_t rows = (p.n + 127) / 128;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
@@ -1014,9 +1016,9 @@ int launch_narrow(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_e
         int n = 0;
         if (resident_clusters(resident[dev][split], kernel, C::THREADS, C::SMEM_BYTES, split, &n)) return GPTQ_ERR_CUDA;
         // (the query counts one CTA that uses TMEM per SM)
-        if (split == STEP || rows * toks <= int64_t(n) * C::PER_SM) break;
+        if (split == STEP || rows <= int64_t(n) * C::PER_SM) break;
     }
-    cfg.gridDim = dim3(unsigned(rows * split), unsigned(toks));
+    cfg.gridDim = dim3(unsigned(rows * split));
     attr[0].val.clusterDim.x = unsigned(split);
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, maps, g) != cudaSuccess) return GPTQ_ERR_CUDA;
@@ -1044,7 +1046,7 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
     fp8::Maps maps;
     std::memset(&maps, 0, sizeof(maps));
     int rc = make_code_map(encode, &maps.w, p.w, p.n, p.d, p.ldw, TN / 2);
-    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldu, TN / 2);
+    if (!rc && GATED) rc = make_code_map(encode, &maps.u, p.u, p.n, p.d, p.ldw, TN / 2);
     if (!rc) rc = make_code_map(encode, &maps.x, p.x, p.m, p.d, p.ldx, 128);
     if (rc) return rc;
     const fp8::Args g{p.m, p.n, p.lds, p.ldy, p.ldys, p.xs, p.ws, p.us, p.y, p.ys, int((p.d + 127) / 128), p.out, st};

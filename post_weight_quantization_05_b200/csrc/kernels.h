@@ -97,7 +97,7 @@ struct Fp8Product {
     const float* us;
     void* y;
     float* ys;
-    int64_t m, n, d, ldx, lds, ldw, ldu, ldy, ldys;
+    int64_t m, n, d, ldx, lds, ldw, ldy, ldys;   // ldw: of both weights
     int out, act;
 };
 int launch_fp8_product(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_encodeTiled encode);
