@@ -9,9 +9,9 @@
 // first pieces while this row's results are formed.  Each of the other threads
 // keeps running sums in base 2,
 //   s = sum 2^z;  t = sum 2^z z;  z = x log2 e - k,  k an integer near the maximum's,
-// moved to a new k (exactly: a power of two) where a piece's maximum lies higher,
-// and the block joins them at the row's end.  A value costs one packed half of each of
-// a multiply-add (z, one rounding), an add and a multiply-add, and one ex2.
+// moved to a new k (exactly: a power of two) where a piece's maximum lies well
+// above, and the block joins them at the row's end.  A value costs one packed half of
+// each of a multiply-add (z, one rounding), an add and a multiply-add, and one ex2.
 // A masked value (-inf) makes 2^z z a NaN: the thread then adds that piece again,
 // and the row's others, with z bounded.  Rows that base 2 cannot hold (values
 // past 1e9, or NaN and infinities) are summed again about their maximum with
@@ -26,12 +26,12 @@
 // a row's latency, not its work, so two more warps do it, every other row each,
 // while the summing warps are in the next row.
 //
-// Measured on a B200: 8192 x 50257 bf16 134 us without alternatives (6.2 TB/s), 149
-// with five, 174 with twenty (163 and 198 when every found value was appended by a
+// Measured on a B200: 8192 x 50257 bf16 136 us without alternatives (6.1 TB/s), 147
+// with five, 172 with twenty (163 and 198 when every found value was appended by a
 // ballot of its own; 235 with five when the summing threads did it; finer maxima,
-// per half piece, 182); 8192 x 50304 fp32 with five 234 us (7.0 TB/s); one row of
-// 128000 fp32 5.1, 7.5 and 13.0 us with none, one and twenty, which is latency: the
-// block's joins and the cluster's.
+// per half piece, 182); 8192 x 50304 fp32 with five 238 us (6.9 TB/s); one row of
+// 128000 fp32 5.4, 7.9 and 13.3 us with none, one and twenty, which is latency: the
+// block's joins, the look at the found values again and the cluster's joins.
 //
 // A row is one block's, or, when there are fewer rows than the GPU has room
 // for, a cluster's: its blocks take turns in the row's pieces, and the first joins
@@ -186,13 +186,13 @@ __device__ __forceinline__ void add_guarded(Sums2& a, float x) {   // a.k is not
 }
 // This thread's `count` vectors of a piece, THREADS apart, into its sums; returns
 // their maximum.  t = sum 2^z z loses as many bits as the z of the values that
-// count are large, so k follows the maximum: it moves to a piece's once that is
-// added, and if that lies RISE or more above it, first, the piece added again.
-// (With k left 60 behind, 50257 equal logits 40 above the first piece's had an
-// entropy 1.5e-4 off; 5e-6 at most now.  A smaller RISE adds more pieces
-// twice: 8192 x 50257 bf16 with five alternatives 149 us for none, 150 for 16, 152
-// for 8.)  guarded: a masked value has been met.
-constexpr float RISE = 16.0f;
+// count are large, so k follows the maximum: where a piece's lies more than NEAR
+// above k, k moves to it once the piece is added, and where it lies RISE above,
+// first, the piece added again.  (With k left 60 behind, 50257 equal logits 40 above
+// the first piece's had an entropy 1.5e-4 off; 5e-6 at most now.  8192 x 50257 bf16
+// with no and with five alternatives: 135 and 147 us; 141 and 153 with NEAR = 0, two
+// more with RISE = 8.)  guarded: a masked value has been met.
+constexpr float NEAR = 6.0f, RISE = 16.0f;
 template <typename T>
 __device__ __forceinline__ float add_piece(Sums2& a, bool& guarded, const uint4* at, int count) {
     Top<T> top;
@@ -228,17 +228,21 @@ __device__ __forceinline__ float add_piece(Sums2& a, bool& guarded, const uint4*
         fp8::unpack2(t, t0, t1);
         fp8::unpack2(s, s0, s1);
         m = top.value();
-        const float k = ceilf(m * LOG2E);
-        guarded = t0 + t1 != t0 + t1;
-        if (guarded || (pass == 0 && fmaf(m, LOG2E, -a.k) >= RISE)) {
-            if (k > a.k) move_to(a, k);
-            continue;
-        }
+        const float rise = fmaf(m, LOG2E, -a.k);
         Sums2 piece{a.k, s0 + s1, t0 + t1};
+        guarded = piece.t != piece.t;
+        if (!guarded && rise <= NEAR) {
+            a.s += piece.s;
+            a.t += piece.t;
+            return m;
+        }
+        const float k = ceilf(m * LOG2E);
+        const bool again = guarded || (pass == 0 && rise >= RISE);
         if (k > a.k) {
             move_to(piece, k);
             move_to(a, k);
         }
+        if (again) continue;
         a.s += piece.s;
         a.t += piece.t;
         return m;
