@@ -66,8 +66,18 @@ class Fp8Linear(_Fp8Module):
     """nn.Linear's product from the 8-bit form; outputs in the inputs' type
     (fp32, bf16 or fp16)."""
 
+    @staticmethod
+    def check(linear: nn.Linear):
+        """Raises ValueError if `linear` has no 8-bit form."""
+        w = linear.weight
+        if not w.is_cuda or w.dtype not in (torch.float32, torch.bfloat16, torch.float16) or not (
+                1 <= w.shape[0] <= 1 << 22 and 1 <= w.shape[1] <= 1 << 18):
+            raise ValueError("the 8-bit form needs a weight of fp32, bf16 or fp16 on a GPU, of at most 2^22 x 2^18, "
+                             f"got {tuple(w.shape)} of {w.dtype} on {w.device}")
+
     def __init__(self, linear: nn.Linear):
         super().__init__()
+        self.check(linear)
         self.out_features, self.in_features = linear.weight.shape
         self._add_weight("codes", linear.weight)
         self.register_buffer("bias", None if linear.bias is None else linear.bias.detach().clone())
@@ -119,27 +129,27 @@ _READS_WEIGHTS = (nn.TransformerEncoderLayer,)
 def quantize_linears(module: nn.Module, exclude=None) -> nn.Module:
     """Replace every nn.Linear inside `module` by its 8-bit form, in place (a
     linear layer itself: the form is returned).  A linear that the module holds
-    in several places keeps doing so, as one form.
+    in several places keeps doing so, as one form.  Either all are replaced or,
+    if one has no such form (ValueError), none.
 
     The form has no `weight`, so a linear whose weight someone else reads has to
     stay: subclasses of nn.Linear do, and those of an nn.TransformerEncoderLayer.
     For others exclude(name, linear) says so by returning True, asked for every
     place that holds a linear, with the place's name as module.named_modules()
     spells it."""
+    def taken(name, linear):
+        if type(linear) is not nn.Linear or (exclude is not None and exclude(name, linear)):
+            return False
+        Fp8Linear.check(linear)
+        return True
+    if type(module) is nn.Linear:
+        return Fp8Linear(module) if taken("", module) else module
+    places = [(parent, name, child)
+              for prefix, parent in module.named_modules() if not isinstance(parent, _READS_WEIGHTS)
+              for name, child in parent._modules.items() if taken(f"{prefix}.{name}" if prefix else name, child)]
     forms: dict[nn.Module, Fp8Linear] = {}
-
-    def form(name, linear):
-        if exclude is not None and exclude(name, linear):
-            return linear
+    for parent, name, linear in places:
         if linear not in forms:
             forms[linear] = Fp8Linear(linear)
-        return forms[linear]
-    if type(module) is nn.Linear:
-        return form("", module)
-    for prefix, parent in list(module.named_modules()):
-        if isinstance(parent, _READS_WEIGHTS):
-            continue
-        for name, child in list(parent._modules.items()):
-            if type(child) is nn.Linear:
-                setattr(parent, name, form(f"{prefix}.{name}" if prefix else name, child))
+        setattr(parent, name, forms[linear])
     return module

@@ -60,6 +60,7 @@ def test_shared_memory():
 
 class Form(nn.Module):
     """Stands for Fp8Linear, which needs a GPU."""
+    check = staticmethod(lambda linear: None)
 
     def __init__(self, linear):
         super().__init__()
@@ -98,3 +99,33 @@ def test_excluded_linears_stay(monkeypatch):
     assert sorted(name for name, _ in seen) == ["c", "d", "inner.a", "inner.b"]
     lin = nn.Linear(4, 4)
     assert fp8.quantize_linears(lin, exclude=lambda name, _: name == "") is lin
+
+
+def test_a_model_is_replaced_whole_or_not_at_all(monkeypatch):
+    """A linear that has no 8-bit form is found before any other is replaced."""
+    class Picky(Form):
+        @staticmethod
+        def check(linear):
+            if linear.weight.dtype == torch.float64:
+                raise ValueError("no")
+    monkeypatch.setattr(fp8, "Fp8Linear", Picky)
+    m = nn.Sequential(nn.Linear(8, 8), nn.Linear(8, 8).double())
+    with pytest.raises(ValueError):
+        fp8.quantize_linears(m)
+    assert type(m[0]) is nn.Linear and type(m[1]) is nn.Linear
+    fp8.quantize_linears(m, exclude=lambda name, linear: name == "1")
+    assert isinstance(m[0], Picky) and type(m[1]) is nn.Linear
+
+
+@pytest.mark.parametrize("linear", [nn.Linear(8, 8), nn.Linear(8, 8, dtype=torch.float64),
+                                    nn.Linear(8, 8, device="meta")])
+def test_linears_without_a_form(linear):
+    """Weights off the GPU or of another type are refused."""
+    with pytest.raises(ValueError):
+        fp8.Fp8Linear.check(linear)
+    with pytest.raises(ValueError):
+        fp8.quantize_linears(linear)
+    m = nn.ModuleList([linear])
+    with pytest.raises(ValueError):
+        fp8.quantize_linears(m)
+    assert m[0] is linear
