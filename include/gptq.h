@@ -370,7 +370,8 @@ int gptq_dequantize(const uint32_t* codes, const uint16_t* scales, const uint16_
  *       token (weights: the block's first row) as its detail.
  *
  * Here rows may be pitched and no size need be a multiple of anything:
- *   dtype   GPTQ_F32, GPTQ_BF16 or GPTQ_F16 (x, W), aligned to its size.
+ *   dtype   GPTQ_F32, GPTQ_BF16 or GPTQ_F16 (x, W), aligned to its size (rows
+ *           that all begin on 16-byte boundaries are up to eight times as fast).
  *   ldx, ldw    elements between rows, >= d_in.
  *   codes   uint8 e4m3 bit patterns, 16-byte aligned; ldc bytes between rows,
  *           a multiple of 16, >= d_in.  The bytes of a row behind d_in are not
@@ -413,7 +414,8 @@ int gptq_fp8_quantize_weight(const void* W, int dtype, int64_t d_out, int64_t d_
  *           to its type's size (codes: as above).
  *   ys      GPTQ_FP8: scales of h, [ceil(d_out / 128), m], pitch ldys >= m;
  *           otherwise NULL.
- *   act     0: silu, g / (1 + e^-g).  1: gelu, g Phi(g) (the exact form).
+ *   act     0: silu, g / (1 + e^-g), 0 for g below -87.3 (where the formula's
+ *           magnitude is below 2^-119).  1: gelu, g Phi(g) (the exact form).
  * Sizes and overlaps as above.  The first call of a kind sets its kernels up:
  * a caller that records these calls (or the quantizers, or the token scores)
  * into a stream capture makes one such call before the capture begins.

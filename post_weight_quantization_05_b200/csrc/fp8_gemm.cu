@@ -140,9 +140,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 
 // act(g): SILU, g / (1 + e^-g); GELU in its exact form, g Phi(g), with Phi
-// from erfc so that large negative gates keep their relative accuracy.  The
-// reciprocal of e^88 is below the normal numbers and counts as 0.
-// (The clamps keep exp_of's products finite.)
+// from erfc so that large negative gates keep their relative accuracy.  Silu of
+// gates below -87.3 is 0: the reciprocal is below the normal numbers there (the
+// formula's value is below 2^-119).  (The clamps keep exp_of's products finite.)
+// 4096 tokens, a pair of 11008 x 4096: 344 us with silu, 407 with gelu, whose erfc is
+// in the tiles' output with nothing beside it.
 constexpr int SILU = 0, GELU = 1;
 template <int ACT>
 __device__ __forceinline__ float gate_act(float g) {
@@ -445,9 +447,10 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
 // block's MMAs.  (The sums' warps did it themselves before, 270 of a block's
 // clocks: 4096 tokens, a pair of 11008 x 4096, 393 us then, 343 now.)
 //
-// Measured: 4096 tokens, 8192 x 28672 822 us (2340 TFLOP/s; 948 before the MMAs
-// were issued by an elected thread), 8192 x 4096 126 us.  A block takes some 800
-// clocks, not 512.  What is in the way is the whole circle of an accumulator --
+// Measured: 4096 tokens, 8192 x 28672 814 to 847 us from box to box (2270 to 2360
+// TFLOP/s; 948 before the MMAs were issued by an elected thread), 8192 x 4096 128
+// us; calls that follow one another without a pause take up to 990 under the power
+// cap.  A block takes some 800 clocks, not 512.  What is in the way is the whole circle of an accumulator --
 // MMAs, their arrival, 128 KB read from TMEM and 32768 multiply-adds, the arrival
 // back -- and power: without the sums' reads and multiply-adds the same kernel
 // takes 680 us.  Tried and slower: 128 columns per MMA and accumulator, released
@@ -457,7 +460,9 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
 // Two variations fit fewer tiles to the GPU: TN = 128 (half the weight rows, four
 // accumulators), and SPLIT pairs in a cluster that share a tile's blocks of k
 // and add their sums through distributed shared memory, a slice of the columns
-// each, in rank order.
+// each, in rank order.  A block of 128 columns costs nearly what one of 256 does (590
+// clocks, of which 256 are MMAs): the waits, the first TMEM load and the arrivals
+// are the same.
 template <int TN, int SPLIT>
 struct Wide {
     static constexpr int STAGE_BYTES = TILE_BYTES + TN / 2 * 128;
@@ -1075,8 +1080,10 @@ int launch_wide(const Fp8Product& p, cudaStream_t stream, DevStatus* st, PFN_enc
 // The SM-pair form of a product: the tile width and the pairs per tile with the
 // least estimated time,
 //   rounds of tiles x (blocks of k per pair x time of a block + time of a tile),
-// fitted to these measurements (us; 256-wide tiles by 1 pair, 128-wide by 1, 256 by
-// 2, 128 by 2, 128 by 4):
+// which is to rank them, not to tell the time: for the first row below it gives 50
+// us for the 256-wide tile by 2 and 70 for the 128-wide by 1.  Its constants follow
+// these measurements (us; 256-wide tiles by 1 pair, 128-wide by 1, 256 by 2, 128 by
+// 2, 128 by 4):
 //   256 tokens, 8192 x 28672    94.7   72.7   64.8   81.3   117
 //   256 tokens, 4096 x 4096     19.3   13.5   16.0   12.5   29.1
 //   512 tokens, 11008 x 4096    36.0   33.5   48.5   68.1   115
@@ -1120,7 +1127,10 @@ int choose_wide(const Fp8Product& p, WideChoice* out) {
 }
 
 // Up to this many tokens a product runs with the weights on the MMA's M side: 32
-// tokens, 8192 x 28672 41 us against 56 on SM pairs, 11008 x 4096 13.7 against 19.
+// tokens, 8192 x 28672 41 us against 59 on SM pairs, 11008 x 4096 13.8 against 20.
+// The next token pays that step.  Tiles of 64 and 128 tokens with the weights on the
+// M side were slower than SM pairs except for the largest weight (64 tokens, 8192 x
+// 28672: 50 us against 56), measured with one block of k a stage.
 constexpr int64_t kNarrowTokens = 32;
 
 template <int ACT>

@@ -8,8 +8,15 @@
 // codes, so each value is read once and one byte is written for it.  The
 // bound is HBM: 3 bytes a value (bf16) or 5 (fp32).  Measured: rows 8192 x 11008
 // bf16 53 us (5.1 TB/s; 103 with a division per value, 74 with a branch for the
-// quotients next to a middle), weight 8192 x 28672 bf16 129 us (5.4 TB/s): reads
-// and writes mixed, and the coder's issue slots behind them.
+// quotients next to a middle), fp32 69 us (6.6 TB/s); weight 8192 x 28672 bf16 131
+// us (5.4 TB/s), fp32 195: reads and writes mixed, and in 16 bits the coder's issue
+// slots behind them.
+//
+// That is for rows on 16-byte boundaries of at least a warp's 1024 channels.  The
+// forms for any alignment are right but far from HBM: rows 8192 x 11008 at an odd
+// pitch 127 us in bf16 and 105 in fp32, a weight of 3021 x 22881 bf16 327 us (22880
+// columns, aligned: 43) and fp32 79.  Of rows of 128 channels seven warps' loads in
+// eight are empty: 65536 of them in bf16 take 33 us, 8 times their bytes' time.
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -127,7 +134,8 @@ __global__ void __launch_bounds__(32 * WARPS)
 }
 
 // Rows at any alignment: a warp takes whole blocks, lane l the values l, l + 32,
-// l + 64 and l + 96 of each, so loads and byte stores are still contiguous.
+// l + 64 and l + 96 of each: a warp's loads and stores are contiguous, but of one
+// value a lane, and the codes leave a byte at a time.
 template <typename T>
 __global__ void __launch_bounds__(32 * WARPS)
     quant_rows_any_kernel(const T* __restrict__ x, int64_t m, int64_t d, int64_t ldx, uint8_t* __restrict__ codes,
@@ -214,7 +222,8 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// The same at any alignment: columns lane, lane + 32, ... of every eighth row.
+// The same at any alignment: columns lane, lane + 32, ... of every eighth row, one
+// value a load and one byte a store.
 template <typename T>
 __global__ void __launch_bounds__(256)
     quant_weight_any_kernel(const T* __restrict__ w, int64_t n, int64_t d, int64_t ldw, uint8_t* __restrict__ codes,

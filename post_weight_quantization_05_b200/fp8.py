@@ -4,6 +4,9 @@ inference: torch modules over api.fp8_quantize_weight, fp8_quantize_rows,
 fp8_gemm and fp8_gated.  A weight is quantized once, when the layer is made;
 each call quantizes its inputs, a scale per token and 128 channels, and
 multiplies codes with codes.  The float weights are not kept.
+
+A weight or an input that holds a NaN or an infinity is recorded in the library's
+status word (a token's outputs are then NaN): api.get_status() reads and clears it.
 """
 from __future__ import annotations
 
