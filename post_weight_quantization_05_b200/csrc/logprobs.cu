@@ -26,11 +26,11 @@
 // a row's latency, not its work, so two more warps do it, every other row each,
 // while the summing warps are in the next row.
 //
-// Measured on a B200: 8192 x 50257 bf16 136 us without alternatives (6.1 TB/s), 147
-// with five, 172 with twenty (163 and 198 when every found value was appended by a
+// Measured on a B200: 8192 x 50257 bf16 135 us without alternatives (6.1 TB/s), 147
+// with five, 171 with twenty (163 and 198 when every found value was appended by a
 // ballot of its own; 235 with five when the summing threads did it; finer maxima,
 // per half piece, 182); 8192 x 50304 fp32 with five 238 us (6.9 TB/s); one row of
-// 128000 fp32 5.4, 7.9 and 13.3 us with none, one and twenty, which is latency: the
+// 128000 fp32 5.2, 7.5 and 12.8 us with none, one and twenty, which is latency: the
 // block's joins, the look at the found values again and the cluster's joins.
 //
 // A row is one block's, or, when there are fewer rows than the GPU has room
