@@ -439,7 +439,7 @@ int gptq_fp8_gated(const uint8_t* x, int64_t ldx, const float* xs, int64_t lds, 
  *   logp[i]     = ln p[targets[i]]; 0 for a negative target (a position that
  *                 is not scored).  A target >= vocab is recorded as
  *                 GPTQ_ERR_INVALID_ARG (detail: the row) and gives NaN.
- *   entropy[i]  = - sum p ln p (may be NULL)
+ *   entropy[i]  = - sum p ln p (may be NULL).  At least 0, and logp at most 0.
  *   top_ids[i], top_logp[i]   the `top` largest p in descending order, equal
  *                 ones by increasing index.
  *   logits  device [n, vocab] of dtype (GPTQ_F32, GPTQ_BF16, GPTQ_F16), ld

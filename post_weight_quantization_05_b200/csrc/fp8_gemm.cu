@@ -447,15 +447,16 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, Narrow<NT>::PER_SM)
 // block's MMAs.  (The sums' warps did it themselves before, 270 of a block's
 // clocks: 4096 tokens, a pair of 11008 x 4096, 393 us then, 343 now.)
 //
-// Measured: 4096 tokens, 8192 x 28672 814 to 847 us from box to box (2270 to 2360
+// Measured: 4096 tokens, 8192 x 28672 814 to 847 us from GPU to GPU (2270 to 2360
 // TFLOP/s; 948 before the MMAs were issued by an elected thread), 8192 x 4096 128
 // us; calls that follow one another without a pause take up to 990 under the power
-// cap.  A block takes some 800 clocks, not 512.  What is in the way is the whole circle of an accumulator --
-// MMAs, their arrival, 128 KB read from TMEM and 32768 multiply-adds, the arrival
-// back -- and power: without the sums' reads and multiply-adds the same kernel
-// takes 680 us.  Tried and slower: 128 columns per MMA and accumulator, released
-// one by one, with one issuing warp or two (1110 us: A is read twice), sixteen
-// warps for the sums.  (Stages: three to six of 32 KB measured the same.)
+// cap.  A block takes some 800 clocks, not 512.  What is in the way is the whole
+// circle of an accumulator -- MMAs, their arrival, 128 KB read from TMEM and 32768
+// multiply-adds, the arrival back -- and power: without the sums' reads and
+// multiply-adds the same kernel takes 680 us.  Tried and slower: 128 columns per MMA
+// and accumulator, released one by one, with one issuing warp or two (1110 us: A is
+// read twice), sixteen warps for the sums.  (Stages: three to six of 32 KB measured
+// the same.)
 //
 // Two variations fit fewer tiles to the GPU: TN = 128 (half the weight rows, four
 // accumulators), and SPLIT pairs in a cluster that share a tile's blocks of k

@@ -15,8 +15,8 @@
 // That is for rows on 16-byte boundaries of at least a warp's 1024 channels.  The
 // forms for any alignment are right but far from HBM: rows 8192 x 11008 at an odd
 // pitch 127 us in bf16 and 105 in fp32, a weight of 3021 x 22881 bf16 327 us (22880
-// columns, aligned: 43) and fp32 79.  Of rows of 128 channels seven warps' loads in
-// eight are empty: 65536 of them in bf16 take 33 us, 8 times their bytes' time.
+// columns, aligned: 43) and fp32 79.  Of rows of 128 channels seven eighths of
+// a warp's loads are empty: 65536 of them in bf16 take 33 us, 8 times their bytes'.
 #include "fp8.cuh"
 #include "kernels.h"
 
